@@ -36,10 +36,13 @@ def listed():
         # a long prompt of a model with interleaved pairs, half of each head rotated, positions stretched
         {"name": "rope_chunk_8192", "op": "rope", "tokens": 8192, "nq": 64, "nkv": 8, "d": 128, "rot": 64,
          "interleaved": True, "factor": 8.0, "far": 131072, "in": "bf16", "out": "bf16"},
-        # one new token for each decode request, into pages that hold older slots
-        {"name": "append_decode_512", "op": "append", "tokens": 512, "nkv": 8, "d": 128, "run": 1, "in": "f32"},
+        # one new token for each decode request, into pages that hold older slots: k as the rotation leaves it, v as
+        # the QKV product does
+        {"name": "append_decode_512", "op": "append", "tokens": 512, "nkv": 8, "d": 128, "run": 1, "k": "bf16",
+         "v": "f32"},
         # a prompt: whole pages in a row
-        {"name": "append_chunk_8192", "op": "append", "tokens": 8192, "nkv": 8, "d": 128, "run": 1024, "in": "bf16"},
+        {"name": "append_chunk_8192", "op": "append", "tokens": 8192, "nkv": 8, "d": 128, "run": 1024, "k": "bf16",
+         "v": "bf16"},
         # a short cached prefix of the tiny layer, an odd number of rows
         {"name": "read_prefix_45", "op": "read", "tokens": 45, "nkv": 2, "d": 64, "run": 45, "out": "f32"},
         # cached prefixes of a batch, for attention of new prompts over them
@@ -79,7 +82,8 @@ def draw(rng):
     if op in ("append", "read"):
         T = _log_int(rng, 1, 8192 if op == "append" else 32768)
         c = {"op": op, "tokens": T, "nkv": nkv, "d": d, "run": min(T, rng.choice([1, 7, 100, 1024]))}
-        c["in" if op == "append" else "out"] = rng.choice(["f32", "bf16"])
+        for name in ("k", "v") if op == "append" else ("out",):
+            c[name] = rng.choice(["f32", "bf16"])
         return c
     R = _log_int(rng, 1, 512)
     most = min(131072, 512 * 1536 * 8 * 128 // (R * nkv * d))
@@ -134,7 +138,8 @@ def work(case):
         return {"bytes": T * (heads * case["d"] * size + 4) + 4 * case["rot"], "flops": 3 * T * heads * case["rot"]}
     n, held = _rows(case) if op != "attn" else (0, 0)
     if op == "append":  # rows in, codes written and read back, rows out
-        return {"bytes": case["tokens"] * (n * (4 if case["in"] == "f32" else 2) + 2 * held + 2 * n + 4),
+        size = sum(4 if case[k] == "f32" else 2 for k in ("k", "v"))
+        return {"bytes": case["tokens"] * (n // 2 * size + 2 * held + 2 * n + 4),
                 "flops": 4 * case["tokens"] * n}
     if op == "read":
         return {"bytes": case["tokens"] * (held + n * (4 if case["out"] == "f32" else 2) + 4),
@@ -315,9 +320,8 @@ def prepare(case, seed):
         out = torch.bfloat16 if op == "append" else DTYPES[case["out"]][0]
         s["k"], s["v"] = (torch.empty((T, nkv, d), dtype=out, device="cuda") for _ in range(2))
         if op == "append":  # k rotated and on its own, v beside q and k in the product's rows
-            dt = DTYPES[case["in"]][0]
-            s["new_k"] = _normal(gen, (T, nkv, d), dt)
-            s["new_v"] = _normal(gen, (T, 6 * nkv, d), dt)[:, 5 * nkv:]
+            s["new_k"] = _normal(gen, (T, nkv, d), DTYPES[case["k"]][0])
+            s["new_v"] = _normal(gen, (T, 6 * nkv, d), DTYPES[case["v"]][0])[:, 5 * nkv:]
     else:
         lens = _lengths(case)
         R, nq, nkv, d = case["requests"], case["nq"], case["nkv"], case["d"]
@@ -429,8 +433,8 @@ def _own(s):
     elif op in ("append", "read"):
         if op == "append":
             nf.check(nf.nf_op_kv4_append(
-                s["new_k"].data_ptr(), s["new_k"].stride(0), s["new_v"].data_ptr(), s["new_v"].stride(0),
-                DTYPES[c["in"]][1], s["slots"].data_ptr(), c["tokens"], s["pool"].data_ptr(), s["pages"], nkv, d,
+                s["new_k"].data_ptr(), s["new_k"].stride(0), DTYPES[c["k"]][1], s["new_v"].data_ptr(),
+                s["new_v"].stride(0), DTYPES[c["v"]][1], s["slots"].data_ptr(), c["tokens"], s["pool"].data_ptr(), s["pages"], nkv, d,
                 status, stream))
         nf.check(nf.nf_op_kv4_read(
             s["pool"].data_ptr(), s["pages"], s["slots"].data_ptr(), c["tokens"], nkv, d, s["k"].data_ptr(), nkv * d,
