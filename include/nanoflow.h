@@ -469,6 +469,150 @@ nf_status nf_decode_attention_noalloc(const void* q, void* out, const void* kv_p
                                       int32_t n_kv_heads, int32_t head_dim, int32_t sm_count,
                                       int32_t* status_device, void* stream);
 
+/* ------------------------------------------------------------------ 4-bit KV cache
+ *
+ * One decode step over a paged cache held in 4 bits, as single operations: page tables and slots of the
+ * batch (nf_op_page_map), rotary positions (nf_op_rope), the new rows of K and V into the cache
+ * (nf_op_kv4_append) and paged GQA decode attention over it (nf_op_kv4_decode_attention); rows read back
+ * (nf_op_kv4_read). The rows of q, k and v may come from nf_op_gemm_bf16 (fp32), the attention output goes
+ * to it (bf16).
+ *
+ * The cache. A pool of num_pages pages of 16 slots for one layer (nf_kv4_page_bytes each, 16-byte
+ * aligned); slot id = page * 16 + slot. K and V are kept as codes of 4 bits with one bf16 scale per slot, KV
+ * head and 32 columns (4.5 bits an element): a = max |x| of the 32 values rounded to bf16, scale = a / 7
+ * rounded to bf16, code = x / scale rounded half to even (-7..7), value = code * scale. Groups with
+ * a < 2^-60 are held as zeros; groups with a > 2^60, an infinity or a NaN read back as NaN throughout.
+ * A page holds, per KV head, a K tile and a V tile of 9 d bytes: 8 d bytes of codes (code + 8, two to a
+ * byte), then 16 x d / 32 bf16 scales [slot][group]. With p % 2 choosing the low or high half of the byte:
+ *   K, slot s, column 32 j + 8 t + 2 p + h:       byte s d/2 + t d/8 + 4 j + 2 h + p / 2
+ *   V, slot 8 e + 2 t + h, column 32 j + 4 g + p: byte e 4d + t d + g d/8 + 4 j + 2 h + p / 2
+ * (p in 0..3, h in 0..1, t in 0..3, g in 0..7). No two slots share a byte. A pool needs no initial value:
+ * slots that were never written are never read by a request whose length does not cover them.
+ *
+ * Common to these calls: device pointers of the current device (or managed memory; anything else is
+ * NF_ERR_INVALID_ARGUMENT), row strides in elements between consecutive tokens, head h of a row at column
+ * h * head_dim. `status_device` (required) is an int32 that the caller zeroes; it receives the first error
+ * that the device finds. All are asynchronous on `stream`, allocate nothing and may be captured into CUDA
+ * graphs. NF_ERR_UNSUPPORTED for head dims other than 64 and 128, more than 256 KV heads or more than 8
+ * query heads per KV head (nf_op_rope: head dims above 512, more than 65536 heads). */
+
+#define NF_DTYPE_BF16 0
+#define NF_DTYPE_F32 1
+#define NF_KV4_MAX_REQUESTS 16384   /* requests of one call at most */
+#define NF_KV4_MAX_PAGES 134217727  /* pages of a pool at most: slot ids fit an int32 */
+
+/* Page tables, slots and positions of a batch from its request lengths. Request r has ctx_len[r] cached
+ * tokens and new_len[r] new ones (new_len NULL: one each); b = ceil(ctx_len / 16) pages of its row of
+ * block_table [num_requests x table_stride] are in use, and its new tokens need a - b more,
+ * a = ceil((ctx_len + new_len) / 16). These are taken from the end of free_pages, in request order: the
+ * k-th page taken is free_pages[free_count[0] - 1 - k]. Written are
+ *   block_table   the new entries, columns b .. a - 1 of each row (others stay as they are);
+ *   kv_len        [num_requests] ctx_len + new_len;
+ *   page_indptr   [num_requests + 1], page_indices: the CSR page table of the a pages of each request;
+ *   slots, positions  one entry per new token, request after request: its slot id and its position
+ *                 (ctx_len[r] + i); entries behind the last token stay as they are;
+ *   free_left     free_count[0] less the pages taken (a word of its own, free_left == free_count is refused;
+ *                 pass it as free_count of the next step).
+ * free_pages holds free_cap entries, page_indices page_cap, slots and positions token_cap each.
+ * A request is refused when its new pages, with those of all requests before it, exceed free_count
+ * (NF_ERR_OUT_OF_MEMORY latched), or when ceil((ctx_len + new_len) / 16) > table_stride
+ * (NF_ERR_DEVICE_BOUNDS): it takes no page, keeps kv_len = ctx_len and its old pages, and its tokens get
+ * slot -1 (which nf_op_kv4_append skips). Also NF_ERR_DEVICE_BOUNDS: a negative length (read as an empty
+ * request without new tokens), ceil(ctx_len / 16) > table_stride (kv_len 0, no page, slots -1), a page
+ * id outside [0, num_pages) (copied to the tables as it is, its tokens get slot -1), free_count outside
+ * [0, free_cap] (clamped), and a batch of more pages than page_cap or tokens than token_cap: nothing is taken,
+ * kv_len and page_indptr are 0 and all slots -1 (positions and page_indices stay as they are). */
+nf_status nf_op_page_map(const int32_t* ctx_len, const int32_t* new_len, int32_t num_requests, int32_t* block_table,
+                         int32_t table_stride, const int32_t* free_pages, int32_t free_cap, const int32_t* free_count,
+                         int32_t num_pages, int32_t* kv_len, int32_t* page_indptr, int32_t* page_indices,
+                         int32_t page_cap, int32_t* slots, int32_t* positions, int32_t token_cap, int32_t* free_left,
+                         int32_t* status_device, void* stream);
+
+/* Frequencies of rotary positions. With f_i = theta^(-2 i / rot_dim), i < rot_dim / 2:
+ *   NF_ROPE_PLAIN       f_i
+ *   NF_ROPE_LINEAR      f_i / factor (positions interpolated)
+ *   NF_ROPE_NTK         theta replaced by theta * factor^(rot_dim / (rot_dim - 2))
+ *   NF_ROPE_WAVELENGTH  by the turns n = original_positions * f_i / (2 pi): n <= low turns factor times slower,
+ *                       n >= high as before, between them blended linearly in n
+ *   NF_ROPE_YARN        blended between the same two in the pair index i, from floor and ceil of the
+ *                       (real) indices whose waves turn `high` and `low` times over original_positions; cos and
+ *                       sin scaled by 0.1 ln(factor) + 1
+ * Writes rot_dim / 2 doubles to the host array inv_freq and the factor of cos and sin (1 but for
+ * NF_ROPE_YARN). Host only. NF_ERR_INVALID_ARGUMENT for a null pointer, rot_dim odd, below 2 or above
+ * 512, theta <= 0 (NF_ROPE_YARN: <= 1), factor < 1 where it is used, NF_ROPE_NTK with rot_dim 2,
+ * original_positions < 1 or not 0 < low < high where they are used, or an unknown scaling. */
+enum { NF_ROPE_PLAIN = 0, NF_ROPE_LINEAR = 1, NF_ROPE_NTK = 2, NF_ROPE_WAVELENGTH = 3, NF_ROPE_YARN = 4 };
+
+typedef struct {
+    float theta;
+    int32_t rot_dim;
+    int32_t scaling;            /* NF_ROPE_* */
+    float factor;               /* every scaling but NF_ROPE_PLAIN */
+    float low, high;            /* turns over original_positions (NF_ROPE_WAVELENGTH, NF_ROPE_YARN) */
+    int32_t original_positions; /* (NF_ROPE_WAVELENGTH, NF_ROPE_YARN) */
+} nf_rope_config;
+
+nf_status nf_rope_frequencies(const nf_rope_config* cfg, double* inv_freq, float* cos_sin_scale);
+
+/* Rotate the first rot_dim columns of every head of q and k to their tokens' positions; columns behind them
+ * pass through. Pair i of a head, (x, y) at columns (2 i, 2 i + 1) when interleaved is 1 and
+ * (i, i + rot_dim / 2) when 0, becomes (x c - y s, y c + x s), c and s the cosine and sine of
+ * positions[t] * inv_freq[i] (angle formed in 64 bits) times cos_sin_scale.
+ *   q, q_out   rows [num_tokens] of n_q_heads heads, in_dtype and out_dtype (NF_DTYPE_*); n_q_heads may be 0
+ *   k, k_out   the same for n_kv_heads heads
+ *   positions  device int32 [num_tokens];  inv_freq  device double [rot_dim / 2]
+ * Each side may be rotated in place (same pointer, stride and dtype; other overlaps are not allowed).
+ * Arithmetic in fp32, rounded once. NF_ERR_INVALID_ARGUMENT for null pointers, odd head_dim or rot_dim,
+ * rot_dim > head_dim, interleaved other than 0 and 1, row strides below heads * head_dim, pointers not
+ * aligned to their elements, an in-place side whose strides or dtypes differ. No status word: nothing is indexed
+ * by what the device holds. */
+nf_status nf_op_rope(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t n_q_heads,
+                     const void* k, int64_t k_stride, void* k_out, int64_t k_out_stride, int32_t n_kv_heads,
+                     int32_t in_dtype, int32_t out_dtype, const int32_t* positions, int32_t num_tokens,
+                     int32_t head_dim, int32_t rot_dim, int32_t interleaved, const double* inv_freq,
+                     float cos_sin_scale, void* stream);
+
+/* Bytes of one page of a 4-bit pool, or a negative nf_status. Host only. */
+int64_t nf_kv4_page_bytes(int32_t n_kv_heads, int32_t head_dim);
+
+/* Write num_tokens rows of K and V (k_dtype and v_dtype; [n_kv_heads x head_dim] each) to the slots of a 4-bit pool.
+ * slots[t] = -1 skips the row; any other id outside the pool latches NF_ERR_DEVICE_BOUNDS and is
+ * skipped. The slots of one call must differ (two rows written to one slot may leave a mixture of both).
+ * Strides are multiples of 4 elements and k and v aligned to 4 elements, else NF_ERR_INVALID_ARGUMENT. */
+nf_status nf_op_kv4_append(const void* k, int64_t k_stride, int32_t k_dtype, const void* v, int64_t v_stride,
+                           int32_t v_dtype, const int32_t* slots, int32_t num_tokens, void* pool, int32_t num_pages,
+                           int32_t n_kv_heads, int32_t head_dim, int32_t* status_device, void* stream);
+
+/* Read rows back: k_out and v_out (out_dtype) get the values held at slots[t]; rows with slot -1, or an id
+ * outside the pool (NF_ERR_DEVICE_BOUNDS latched), stay as they are. Strides and alignment as for
+ * nf_op_kv4_append. */
+nf_status nf_op_kv4_read(const void* pool, int32_t num_pages, const int32_t* slots, int32_t num_tokens,
+                         int32_t n_kv_heads, int32_t head_dim, void* k_out, int64_t k_stride, void* v_out,
+                         int64_t v_stride, int32_t out_dtype, int32_t* status_device, void* stream);
+
+/* Bytes of the workspace of nf_op_kv4_decode_attention, whatever the batch, or a negative nf_status. Host only. */
+int64_t nf_kv4_workspace_bytes(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim);
+
+/* Decode attention over a 4-bit pool: for each request r and query head h,
+ * out[r][h] = softmax(softmax_scale * q[r][h] K_r^T) V_r over the first kv_len[r] keys of request r (the new
+ * token's among them once it has been appended), K and V of head h / (n_q_heads / n_kv_heads); zeros where
+ * kv_len[r] is 0.
+ *   q, out         bf16 rows [n_q_heads x head_dim], 16-byte aligned, strides multiples of 8 elements
+ *   kv_len         device int32 [num_requests]; page_indptr, page_indices: CSR page table
+ *   softmax_scale  0: 1 / sqrt(head_dim)
+ *   workspace      nf_kv4_workspace_bytes bytes, 256-byte aligned, zeroed by the caller once before its first
+ *                  use; a call leaves it ready for the next one. Calls that may overlap on the GPU (other
+ *                  streams, two captured graphs) need workspaces of their own.
+ *   sm_count       SMs to run on (0 = all)
+ * NF_ERR_DEVICE_BOUNDS is latched for a negative kv_len (read as 0), a kv_len that the request's pages do not
+ * hold (cut to them) and a page id outside the pool (its keys are left out). Scores, softmax statistics and
+ * sums in fp32. */
+nf_status nf_op_kv4_decode_attention(const void* q, int64_t q_stride, void* out, int64_t out_stride, const void* pool,
+                                     int32_t num_pages, const int32_t* kv_len, const int32_t* page_indptr,
+                                     const int32_t* page_indices, int32_t num_requests, int32_t n_q_heads,
+                                     int32_t n_kv_heads, int32_t head_dim, float softmax_scale, void* workspace,
+                                     int64_t workspace_bytes, int32_t* status_device, int32_t sm_count, void* stream);
+
 /* ------------------------------------------------------------------ serving scheduler (host)
  *
  * The CPU control flow around nf_forward_iteration for a stream of requests (prompt, then greedy

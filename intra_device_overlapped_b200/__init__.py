@@ -26,6 +26,10 @@ NF_MAX_NANO = 4
 NF_TEMPLATE_SEQUENTIAL = 0
 NF_TEMPLATE_PIPELINED = 1
 NF_TEMPLATE_PREFILL_ON_GEMM = 2
+NF_DTYPE_BF16, NF_DTYPE_F32 = 0, 1
+NF_ROPE_PLAIN, NF_ROPE_LINEAR, NF_ROPE_NTK, NF_ROPE_WAVELENGTH, NF_ROPE_YARN = 0, 1, 2, 3, 4
+NF_KV4_MAX_REQUESTS = 16384
+NF_KV4_MAX_PAGES = 134217727
 NF_KERNEL_GEMM, NF_KERNEL_DECODE_ATTN, NF_KERNEL_PREFILL_ATTN = 1, 2, 3
 
 _i32, _i64, _u64, _f32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float, ctypes.c_void_p
@@ -104,6 +108,11 @@ class nf_sched_stats(ctypes.Structure):
         return {f: getattr(self, f) for f, _ in self._fields_}
 
 
+class nf_rope_config(ctypes.Structure):
+    _fields_ = [("theta", _f32), ("rot_dim", _i32), ("scaling", _i32), ("factor", _f32), ("low", _f32),
+                ("high", _f32), ("original_positions", _i32)]
+
+
 class nf_op_time(ctypes.Structure):
     _fields_ = [("kind", _i32), ("nano", _i32), ("layer", _i32), ("stream", _i32), ("grid", _i32),
                 ("us", _f32)]
@@ -172,6 +181,17 @@ def _load():
         "nf_decode_attention_noalloc": ([_vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp],
                                         ctypes.c_int),
         "nf_offload_kv": ([_vp, P(_vp), _i32, P(_i32), _i32, _i32, _i32, _vp, _vp], ctypes.c_int),
+        "nf_op_page_map": ([_vp, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp,
+                            _vp, _vp], ctypes.c_int),
+        "nf_rope_frequencies": ([P(nf_rope_config), P(ctypes.c_double), P(_f32)], ctypes.c_int),
+        "nf_op_rope": ([_vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _i32, _i32, _i32,
+                        _i32, _vp, _f32, _vp], ctypes.c_int),
+        "nf_kv4_page_bytes": ([_i32, _i32], _i64),
+        "nf_op_kv4_append": ([_vp, _i64, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _vp], ctypes.c_int),
+        "nf_op_kv4_read": ([_vp, _i32, _vp, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _i32, _vp, _vp], ctypes.c_int),
+        "nf_kv4_workspace_bytes": ([_i32, _i32, _i32], _i64),
+        "nf_op_kv4_decode_attention": ([_vp, _i64, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _f32,
+                                        _vp, _i64, _vp, _i32, _vp], ctypes.c_int),
         "nf_sched_create": ([P(nf_sched_config), P(_vp)], ctypes.c_int),
         "nf_sched_destroy": ([_vp], None),
         "nf_sched_add_request": ([_vp, P(_i32), _i32, _i32, _i32, P(_i64)], ctypes.c_int),
@@ -195,6 +215,8 @@ EXPORTED = ("nf_status_string", "nf_version", "nf_init_model", "nf_set_layer_wei
             "nf_set_trace", "nf_get_trace", "nf_set_timing", "nf_get_op_times", "nf_op_gemm_bf16", "nf_op_decode_attention",
             "nf_offload_kv",
             "nf_op_prefill_attention", "nf_op_wait_flag_test", "nf_op_persistent_wait_test", "nf_decode_attention_noalloc",
+            "nf_op_page_map", "nf_rope_frequencies", "nf_op_rope", "nf_kv4_page_bytes", "nf_op_kv4_append",
+            "nf_op_kv4_read", "nf_kv4_workspace_bytes", "nf_op_kv4_decode_attention",
             "nf_sched_create", "nf_sched_destroy", "nf_sched_add_request", "nf_sched_next", "nf_sched_complete",
             "nf_sched_request_tokens", "nf_sched_get_stats")
 
@@ -373,6 +395,74 @@ def nf_op_wait_flag_test(flag_ptr: int, limit_ns: int, stream: int = 0) -> int:
 
 def nf_op_persistent_wait_test(limit_ns: int, stream: int = 0) -> int:
     return _lib.nf_op_persistent_wait_test(limit_ns, stream)
+
+
+# --- the 4-bit KV cache (see nanoflow.h) ---
+
+def nf_op_page_map(ctx_len_ptr: int, new_len_ptr: int, num_requests: int, block_table_ptr: int, table_stride: int,
+                   free_pages_ptr: int, free_cap: int, free_count_ptr: int, num_pages: int, kv_len_ptr: int,
+                   page_indptr_ptr: int, page_indices_ptr: int, page_cap: int, slots_ptr: int, positions_ptr: int,
+                   token_cap: int, free_left_ptr: int, status_ptr: int, stream: int = 0) -> int:
+    """Page tables, slots and positions of a batch from its request lengths (new_len_ptr 0: one new token each)."""
+    return _lib.nf_op_page_map(ctx_len_ptr, new_len_ptr, num_requests, block_table_ptr, table_stride, free_pages_ptr,
+                               free_cap, free_count_ptr, num_pages, kv_len_ptr, page_indptr_ptr, page_indices_ptr,
+                               page_cap, slots_ptr, positions_ptr, token_cap, free_left_ptr, status_ptr, stream)
+
+
+def nf_rope_frequencies(cfg: nf_rope_config):
+    """Returns (status, [rot_dim / 2 frequencies], factor of cos and sin). Host only."""
+    freq = (ctypes.c_double * max(1, cfg.rot_dim // 2))()
+    scale = _f32()
+    st = _lib.nf_rope_frequencies(ctypes.byref(cfg), freq, ctypes.byref(scale))
+    return st, list(freq), scale.value
+
+
+def nf_op_rope(q_ptr: int, q_stride: int, q_out_ptr: int, q_out_stride: int, n_q_heads: int, k_ptr: int, k_stride: int,
+               k_out_ptr: int, k_out_stride: int, n_kv_heads: int, in_dtype: int, out_dtype: int, positions_ptr: int,
+               num_tokens: int, head_dim: int, rot_dim: int, interleaved: bool, inv_freq_ptr: int,
+               cos_sin_scale: float = 1.0, stream: int = 0) -> int:
+    """Rotary positions on rows of q and k heads (either side may have no heads)."""
+    return _lib.nf_op_rope(q_ptr, q_stride, q_out_ptr, q_out_stride, n_q_heads, k_ptr, k_stride, k_out_ptr,
+                           k_out_stride, n_kv_heads, in_dtype, out_dtype, positions_ptr, num_tokens, head_dim, rot_dim,
+                           interleaved, inv_freq_ptr, cos_sin_scale, stream)
+
+
+def nf_kv4_page_bytes(n_kv_heads: int, head_dim: int) -> int:
+    """Bytes of one page of a 4-bit pool (negative: minus a status)."""
+    return _lib.nf_kv4_page_bytes(n_kv_heads, head_dim)
+
+
+def nf_op_kv4_append(k_ptr: int, k_stride: int, k_dtype: int, v_ptr: int, v_stride: int, v_dtype: int,
+                     slots_ptr: int, num_tokens: int, pool_ptr: int, num_pages: int, n_kv_heads: int, head_dim: int,
+                     status_ptr: int, stream: int = 0) -> int:
+    """Rows of K and V into the slots of a 4-bit pool."""
+    return _lib.nf_op_kv4_append(k_ptr, k_stride, k_dtype, v_ptr, v_stride, v_dtype, slots_ptr, num_tokens, pool_ptr,
+                                 num_pages, n_kv_heads, head_dim, status_ptr, stream)
+
+
+def nf_op_kv4_read(pool_ptr: int, num_pages: int, slots_ptr: int, num_tokens: int, n_kv_heads: int, head_dim: int,
+                   k_out_ptr: int, k_stride: int, v_out_ptr: int, v_stride: int, out_dtype: int, status_ptr: int,
+                   stream: int = 0) -> int:
+    """Rows of K and V read back from the slots of a 4-bit pool."""
+    return _lib.nf_op_kv4_read(pool_ptr, num_pages, slots_ptr, num_tokens, n_kv_heads, head_dim, k_out_ptr, k_stride,
+                               v_out_ptr, v_stride, out_dtype, status_ptr, stream)
+
+
+def nf_kv4_workspace_bytes(n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    """Bytes of nf_op_kv4_decode_attention's workspace (negative: minus a status)."""
+    return _lib.nf_kv4_workspace_bytes(n_q_heads, n_kv_heads, head_dim)
+
+
+def nf_op_kv4_decode_attention(q_ptr: int, q_stride: int, out_ptr: int, out_stride: int, pool_ptr: int, num_pages: int,
+                               kv_len_ptr: int, page_indptr_ptr: int, page_indices_ptr: int, num_requests: int,
+                               n_q_heads: int, n_kv_heads: int, head_dim: int, softmax_scale: float,
+                               workspace_ptr: int, workspace_bytes: int, status_ptr: int, sm_count: int = 0,
+                               stream: int = 0) -> int:
+    """Paged GQA decode attention over a 4-bit pool."""
+    return _lib.nf_op_kv4_decode_attention(q_ptr, q_stride, out_ptr, out_stride, pool_ptr, num_pages, kv_len_ptr,
+                                           page_indptr_ptr, page_indices_ptr, num_requests, n_q_heads, n_kv_heads,
+                                           head_dim, softmax_scale, workspace_ptr, workspace_bytes, status_ptr,
+                                           sm_count, stream)
 
 
 def _i32_array(values) -> "ctypes.Array":

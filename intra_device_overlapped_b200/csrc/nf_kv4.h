@@ -1,0 +1,77 @@
+// The 4-bit paged KV cache: its format, and checks shared by its entry points.
+//
+// A page holds 16 slots of every KV head; per head a K tile, then a V tile, each 9 d bytes: 8 d bytes
+// of codes and 16 x d/32 bf16 scales (value = (code - 8) * scale, one scale per slot and 32 columns).
+// The code order inside a tile is the operand order of the warp-level tensor instruction, so that a lane
+// of the attention kernel finds its operand's codes in consecutive bytes:
+//   K, slot s, column 32 j + 8 t + 2 p + h:       byte s d/2 + t d/8 + 4 j + 2 h + p / 2, nibble p % 2
+//     (the A operand's row s; lane t of a quad holds the pairs h = 0, 1 of both half-steps of group j)
+//   V, slot 8 e + 2 t + h, column 32 j + 4 g + p: byte e 4d + t d + g d/8 + 4 j + 2 h + p / 2, nibble p % 2
+//     (the A operand's column pair t, half e of V^T; p = the rows g, g + 8 of two 16-row tiles)
+// A slot's K codes are d/2 consecutive bytes and its V codes 2-byte units of their own, so that no two
+// slots share a byte and rows can be written in parallel without read-modify-write.
+#pragma once
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "nanoflow.h"
+#include "nf_ptx.cuh"
+
+namespace nf {
+
+constexpr int kKv4Slots = 16;   // slots per page
+constexpr int kKv4Group = 32;   // columns per scale
+constexpr int kKv4MaxHeads = 256;
+
+__host__ __device__ constexpr int kv4_tile_bytes(int d) { return 9 * d; }
+
+// nf_status of a head shape of the 4-bit cache.
+inline nf_status kv4_check_heads(int32_t nkv, int32_t d) {
+    if (nkv < 1 || d < 1) return NF_ERR_INVALID_ARGUMENT;
+    if ((d != 64 && d != 128) || nkv > kKv4MaxHeads) return NF_ERR_UNSUPPORTED;
+    return NF_OK;
+}
+
+inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// NF_OK when every (non-null) pointer is memory of the current device (or managed), else
+// NF_ERR_INVALID_ARGUMENT; NF_ERR_CUDA without a device. A host pointer or another device's
+// would fault in the kernel. No stream operation: allowed while a stream is being captured.
+template <typename... P>
+nf_status check_on_device(const P*... ptrs) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return NF_ERR_CUDA; }
+    const void* list[] = {ptrs...};
+    for (const void* p : list) {
+        if (p == nullptr) continue;
+        cudaPointerAttributes at;
+        if (cudaPointerGetAttributes(&at, p) != cudaSuccess) { cudaGetLastError(); return NF_ERR_CUDA; }
+        if (at.type == cudaMemoryTypeManaged) continue;
+        if (at.type != cudaMemoryTypeDevice || at.device != dev) return NF_ERR_INVALID_ARGUMENT;
+    }
+    return NF_OK;
+}
+
+// Four consecutive values of a bf16 or fp32 row as fp32.
+template <typename T>
+__device__ __forceinline__ float4 load_row4(const void* row, int64_t at) {
+    if constexpr (sizeof(T) == 4) {
+        return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(row) + at));
+    } else {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(row) + at));
+        return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                           __uint_as_float(w.y & 0xFFFF0000u));
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_row4(void* row, int64_t at, float4 v) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(static_cast<float*>(row) + at) = v;
+    } else {
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(row) + at) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    }
+}
+
+}  // namespace nf
