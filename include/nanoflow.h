@@ -606,7 +606,9 @@ int64_t nf_kv4_workspace_bytes(int32_t n_q_heads, int32_t n_kv_heads, int32_t he
  *   sm_count       SMs to run on (0 = all)
  * NF_ERR_DEVICE_BOUNDS is latched for a negative kv_len (read as 0), a kv_len that the request's pages do not
  * hold (cut to them) and a page id outside the pool (its keys are left out). Scores, softmax statistics and
- * sums in fp32. */
+ * sums in fp32; the weights that multiply V, scaled by V's scales, are rounded to fp16 (2^-11). The order of
+ * the sums follows the batch's lengths and sm_count, not the run: equal calls give equal bits. After
+ * NF_ERR_DEVICE_TIMEOUT (a pipeline wait that passed its limit) the workspace has to be zeroed again. */
 nf_status nf_op_kv4_decode_attention(const void* q, int64_t q_stride, void* out, int64_t out_stride, const void* pool,
                                      int32_t num_pages, const int32_t* kv_len, const int32_t* page_indptr,
                                      const int32_t* page_indices, int32_t num_requests, int32_t n_q_heads,

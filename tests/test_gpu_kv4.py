@@ -401,7 +401,10 @@ def _check_attention(c, q, got, scale=None, rows=None):
     scale, rounds to fp16 (2^-11); scores are fp32 sums of q times (code + bias) / 64 in units of 64 scales, 40
     roundings of at most 2^-23 (16-term tensor-core steps cut off) of sums that are at most |q| (|k| + 80 scale) per
     column, and a weight's relative error is twice (numerator, sum) that of its exponent; ex2 adds 2^-22 and the sums
-    2^-22 more."""
+    2^-22 more. A scaled weight w s f, f in [2^8, 2^10) / (the group's largest scale), cannot be nearer than fp16's
+    least step allows, 2^-25: times |code| <= 8, over f and the sum of the weights (at least 1/2: the maximum is the
+    ceiling of a score at most) that is 2^-29 of the group's largest scale for each key, where the keys that weigh most
+    have codes of 0."""
     d, nkv = c.d, c.nkv
     G = q.shape[1] // nkv
     sc = 1.0 / math.sqrt(d) if scale is None else scale
@@ -418,6 +421,8 @@ def _check_attention(c, q, got, scale=None, rows=None):
             unit = np.abs(K[h]).reshape(len(K[h]), -1, 32).max(-1).repeat(32, -1)    # at least a scale, or a zero group
             x_err = 40 * 2.0 ** -23 * sc * (np.abs(qq) @ (np.abs(K[h]) + 80 * unit).T).max(-1)
             bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * x_err[:, None] + 2.0 ** -21) * mass
+            # (some code of a group of 32 is not 0: its largest value is at least its scale)
+            bound += 2.0 ** -29 * len(V[h]) * np.abs(V[h]).max(0).reshape(-1, 32).max(-1).repeat(32)
             err = np.abs(gh[r, h * G:(h + 1) * G] - want)
             assert (err <= bound * (1 + 2.0 ** -6)).all(), (r, h, float((err / bound).max()))
             num, den = num + (err ** 2).sum(), den + (want ** 2).sum()
