@@ -15,12 +15,12 @@ namespace nf {
 namespace {
 
 constexpr int kMaxGroup = 8;               // query heads per KV head: the N = 8 columns of the tensor instruction
-constexpr int kWarps = 4;
+constexpr int kWarps = 12;                 // one CTA per SM, 168 registers a thread (16 warps of 128 spill)
 constexpr int kThreads = kWarps * 32;
-constexpr int kCtasPerSm = 3;              // 12 warps of 168 registers
 constexpr int kStages = 2;                 // pairs of tiles in flight per warp
-constexpr int kMaxCtas = kCtasPerSm * 160; // sizes the workspace (a B200 has 148 SMs)
-constexpr int kMinShare = 8;               // pages of a worker at least
+constexpr int kMaxCtas = 160;              // sizes the workspace (a B200 has 148 SMs)
+constexpr int kMinShare = 16;              // pages of a worker at least
+constexpr int kOverhead = 6;               // what beginning and ending a (request, head) costs, in pages
 constexpr int kMaxParts = 2 * kWarps * kMaxCtas;
 
 struct Kv4AttnArgs {
@@ -50,18 +50,32 @@ struct Item {
 
 __device__ __forceinline__ int part_slot(const Item& it, int c) { return c ? it.slot + 2 * c - 1 : it.slot; }
 
+// How the pages are dealt: every (request, KV head) takes a number of places in one long order, worker w places
+// [w share, (w + 1) share). Warps as workers: a pair takes kOverhead places and one a page. CTAs ("team"): one place for
+// each `chunk` pages or less, and a share is one place.
+struct Deal {
+    int64_t total, share;
+    int chunk;  // 0: warps
+    __device__ __forceinline__ int64_t places(int pages) const {
+        return pages == 0 ? 0 : chunk ? (pages + chunk - 1) / chunk : (int64_t)pages + kOverhead;
+    }
+    __device__ __forceinline__ int worker_of(int64_t pos) const {
+        return (int)((pos | share) >> 32 ? pos / share : (uint32_t)pos / (uint32_t)share);
+    }
+};
+
 template <int D>
 struct Smem {
     static constexpr int kHead = 18 * D;            // K and V tile of a head
     static constexpr int kRow = D + 4;              // merge rows, padded against bank conflicts
-    static constexpr int kHeads = 4 * kThreads / D; // heads joined at a time: a thread has 4 columns of one
     alignas(128) uint8_t ring[kWarps][kStages][2 * kHead];
     alignas(16) uint16_t q[kWarps][2][kMaxGroup * D];
-    float merge[kWarps][kHeads][kRow];
-    Item item[kWarps][2];
+    float merge[kWarps][kMaxGroup][kRow];
+    Item item[kWarps][2], pending[kWarps][2];
     float2 ml[kWarps][kMaxGroup];
     int64_t scan[kWarps], start[kThreads + 1];
-    int last;
+    Deal deal;
+    int last[2];
 };
 
 // Pages that request r reads: its keys, cut to what its row of the page table holds.
@@ -203,48 +217,69 @@ __device__ __forceinline__ void load_words(const uint8_t* at, uint32_t* w) {
 // 2^(m - M) for partial sums: a part without keys (m = -inf) holds zeros, or the NaN of a NaN score
 __device__ __forceinline__ float part_factor(float m, float M) { return m == -INFINITY ? 1.f : ex2_approx(m - M); }
 
-// The whole warp: the stretch that begins at place `pos` of the batch's pages and ends with its (request, head) or with
-// the share, places [worker * share, (worker + 1) * share). Kept out of line: it runs once a stretch and would cost the
-// tile loop registers.
+// The whole warp: the stretch that begins at place `pos` and ends with its (request, head) or at `stop`, the end of the
+// worker's share. Returns the place behind it; a stretch without pages (pos in the overhead before `stop`) has r = -1.
+// Kept out of line: it runs once a stretch and would cost the tile loop registers.
 template <int D>
-__device__ __noinline__ void find_item(const Kv4AttnArgs& a, const Smem<D>& s, int64_t pos, int64_t share, int per,
-                                       Item* out) {
+__device__ __noinline__ int64_t find_item(const Kv4AttnArgs& a, const Smem<D>& s, const Deal& deal, int64_t pos,
+                                          int64_t stop, int worker, int per, Item* out) {
     const int lane = threadIdx.x & 31;
     Item it;
     it.r = -1;
-    // the thread's stretch of requests that holds the place, by 32 and 4 of their starts; then the request
+    int64_t next = stop;
+    // the thread's stretch of requests that holds the place, by 32 and 12 of their starts; then the request
     constexpr int kSub = kThreads / 32;
     int span = (__popc(__ballot_sync(0xffffffffu, s.start[lane * kSub] <= pos)) - 1) * kSub;
-    span += __popc(__ballot_sync(0xffffffffu, lane < kSub && s.start[span + (lane & (kSub - 1))] <= pos)) - 1;
+    span += __popc(__ballot_sync(0xffffffffu, lane < kSub && s.start[span + min(lane, kSub - 1)] <= pos)) - 1;
     int64_t at = s.start[span];
     const int end = min(a.R, (span + 1) * per);
     for (int r = span * per; r < end; r += 32) {
         int keys = 0, pages = 0;
         if (r + lane < end) pages = pages_of(a, r + lane, &keys, false);
-        const int64_t upto = at + warp_prefix((int64_t)pages * a.nkv, lane);
+        int64_t places = deal.places(pages);
+        const int64_t upto = at + warp_prefix(places * a.nkv, lane);
         const uint32_t past = __ballot_sync(0xffffffffu, upto > pos);
         if (past) {
             const int src = __ffs(past) - 1;
             pages = __shfl_sync(0xffffffffu, pages, src);
             keys = __shfl_sync(0xffffffffu, keys, src);
-            const int64_t begin = __shfl_sync(0xffffffffu, upto, src) - (int64_t)pages * a.nkv;
-            it.r = r + src;
-            it.h = (int)((pos - begin) / pages);
-            const int64_t u0 = begin + (int64_t)it.h * pages, u1 = u0 + pages;  // the (request, head)
-            const int w0 = (int)(u0 / share), w = (int)(pos / share);
-            const int b = (int)(pos - u0);
-            it.first = a.indptr[it.r] + b;
-            it.pages = (int)(min(u1, (int64_t)(w + 1) * share) - pos);
-            it.keys = min(keys - b * kKv4Slots, it.pages * kKv4Slots);
-            it.parts = (int)((u1 - 1) / share) - w0 + 1;
-            it.c = w - w0;
-            it.slot = 2 * w0 + 1;
+            places = __shfl_sync(0xffffffffu, places, src);
+            const int64_t begin = __shfl_sync(0xffffffffu, upto, src) - places * a.nkv;
+            int h = -1;  // the last head that begins at or before pos
+            for (int h0 = 0; h0 < a.nkv; h0 += 32)
+                h += __popc(__ballot_sync(0xffffffffu, h0 + lane < a.nkv && begin + (h0 + lane) * places <= pos));
+            const int64_t u0 = begin + h * places;
+            int b, e;  // pages of the stretch
+            if (deal.chunk) {
+                it.parts = (int)places;
+                it.c = (int)(pos - u0);
+                b = (int)((int64_t)pages * it.c / it.parts);
+                e = (int)((int64_t)pages * (it.c + 1) / it.parts);
+                next = pos + 1;
+            } else {
+                const int64_t p0 = u0 + kOverhead, p1 = p0 + pages;
+                b = (int)max(pos - p0, (int64_t)0);
+                e = (int)(min(p1, stop) - p0);  // negative where stop lies in the overhead
+                next = min(p1, stop);
+                const int w0 = pos <= p0 ? worker : deal.worker_of(p0);
+                it.c = worker - w0;
+                it.parts = (p1 <= stop ? worker : deal.worker_of(p1 - 1)) - w0 + 1;
+            }
+            if (b < e) {
+                it.r = r + src;
+                it.h = h;
+                it.first = a.indptr[it.r] + b;
+                it.pages = e - b;
+                it.keys = min(keys - b * kKv4Slots, it.pages * kKv4Slots);
+                it.slot = 2 * (worker - it.c) + 1;
+            }
             break;
         }
         at = __shfl_sync(0xffffffffu, upto, 31);
     }
     if (lane == 0) *out = it;
     __syncwarp();
+    return next;
 }
 
 // 4 columns of a head's output row from its sums
@@ -254,54 +289,55 @@ __device__ __forceinline__ void store_out(const Kv4AttnArgs& a, const Item& it, 
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
-// The parts of a (request, head), joined in order into the output by `warps` warps. A warp takes a head (two of 64
-// columns), 4 columns to a lane; the weights of 32 parts at a time are formed by a lane each, so that the partial rows
-// are all that the threads wait for.
-template <int D>
-__device__ __noinline__ void join_parts(const Kv4AttnArgs& a, const Item& it, int warp, int warps) {
-    constexpr int kAtOnce = 128 / D;
-    const int lane = threadIdx.x & 31, col = lane % (D / 4) * 4;
-    for (int h0 = warp * kAtOnce; h0 < a.G; h0 += warps * kAtOnce) {
-        const int h = h0 + lane / (D / 4);
-        const float* po = a.part_o + (int64_t)min(h, a.G - 1) * D + col;
-        float M[kAtOnce], L[kAtOnce];
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int e = 0; e < kAtOnce; ++e) {
-            M[e] = -INFINITY;
-            L[e] = 0.f;
-            for (int c = lane; c < it.parts; c += 32)
-                M[e] = fmaxf(M[e], __ldcg(a.part_ml + (int64_t)part_slot(it, c) * kMaxGroup + h0 + e).x);
-            for (int of = 16; of; of >>= 1) M[e] = fmaxf(M[e], __shfl_xor_sync(0xffffffffu, M[e], of));
+// Parts of a (request, head), joined in order into the output by one warp: heads h0 .. h0 + H - 1, 4 columns of a head
+// to a lane. The weights of 32 / H parts are formed by a lane each, so that the partial rows are all that the threads
+// wait for; their loads do not depend on one another.
+template <int D, int H>
+__device__ __noinline__ void join_parts(const Kv4AttnArgs& a, const Item& it, int h0) {
+    constexpr int kRows = 128 / D, kAtOnce = 32 / H;  // heads that the lanes cover at a time; parts a round
+    const int lane = threadIdx.x & 31, col = lane % (D / 4) * 4, row = lane / (D / 4);
+    const float2* const ml = a.part_ml + h0 + lane % H;
+    float M = -INFINITY, L = 0.f;
+    for (int c = lane / H; c < it.parts; c += kAtOnce)
+        M = fmaxf(M, __ldcg(ml + (int64_t)part_slot(it, c) * kMaxGroup).x);
+#pragma unroll
+    for (int o = H; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float4 o[H / kRows];
+    const float* po[H / kRows];
+#pragma unroll
+    for (int i = 0; i < H / kRows; ++i) {
+        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        po[i] = a.part_o + (int64_t)min(h0 + i * kRows + row, a.G - 1) * D + col;
+    }
+    for (int c0 = 0; c0 < it.parts; c0 += kAtOnce) {
+        float w = 0.f;
+        if (c0 + lane / H < it.parts) {
+            const float2 m = __ldcg(ml + (int64_t)part_slot(it, c0 + lane / H) * kMaxGroup);
+            w = part_factor(m.x, M);
+            L += w * m.y;
         }
-        for (int c0 = 0; c0 < it.parts; c0 += 32) {
-            float w[kAtOnce];
-            for (int e = 0; e < kAtOnce; ++e) {
-                w[e] = 0.f;
-                if (c0 + lane < it.parts) {
-                    const float2 m = __ldcg(a.part_ml + (int64_t)part_slot(it, c0 + lane) * kMaxGroup + h0 + e);
-                    w[e] = part_factor(m.x, M[e]);
-                    L[e] += w[e] * m.y;
-                }
-            }
-            const int n = min(32, it.parts - c0);
-#pragma unroll 8
-            for (int c = 0; c < n; ++c) {
-                const float4 v =
-                    __ldcg(reinterpret_cast<const float4*>(po + (int64_t)part_slot(it, c0 + c) * a.G * D));
-                float f = __shfl_sync(0xffffffffu, w[0], c);
-                if (kAtOnce > 1) {
-                    const float g = __shfl_sync(0xffffffffu, w[kAtOnce - 1], c);
-                    if (lane >= D / 4) f = g;
-                }
-                o.x += f * v.x;
-                o.y += f * v.y;
-                o.z += f * v.z;
-                o.w += f * v.w;
+        const int n = min(kAtOnce, it.parts - c0);
+#pragma unroll 4
+        for (int c = 0; c < n; ++c) {
+            const int64_t at = (int64_t)part_slot(it, c0 + c) * a.G * D;
+#pragma unroll
+            for (int i = 0; i < H / kRows; ++i) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(po[i] + at));
+                const float f = __shfl_sync(0xffffffffu, w, H * c + i * kRows + row);
+                o[i].x += f * v.x;
+                o[i].y += f * v.y;
+                o[i].z += f * v.z;
+                o[i].w += f * v.w;
             }
         }
-        for (int e = 0; e < kAtOnce; ++e)
-            for (int of = 16; of; of >>= 1) L[e] += __shfl_xor_sync(0xffffffffu, L[e], of);
-        if (h < a.G) store_out(a, it, D, h, col, o, lane < D / 4 ? L[0] : L[kAtOnce - 1]);
+    }
+#pragma unroll
+    for (int of = H; of < 32; of <<= 1) L += __shfl_xor_sync(0xffffffffu, L, of);
+#pragma unroll
+    for (int i = 0; i < H / kRows; ++i) {
+        const int h = i * kRows + row;
+        const float sum = __shfl_sync(0xffffffffu, L, h);
+        if (h0 + h < a.G) store_out(a, it, D, h0 + h, col, o[i], sum);
     }
 }
 
@@ -324,41 +360,60 @@ __device__ __noinline__ void join_parts(const Kv4AttnArgs& a, const Item& it, in
 //   which one vote per two tiles detects. P goes from accumulator to operand layout by movmatrix.
 // Sums and statistics are fp32. M0, M1 etc. belong to the two head columns 2 t, 2 t + 1 of a lane.
 //
-// Work. The pages of all (request, KV head) pairs, in order, are dealt to the workers in equal shares; a share covers
-// some pairs whole and one at either end in part. Each CTA scans the lengths itself (no second launch, nothing on the
-// host depends on them). With many pairs a worker is a warp: no barrier, nothing shared. With at most half as many
-// pairs as CTAs it is a CTA, whose 4 warps take a stretch's pages by twos and join their sums in shared memory
-// ("team"), so that a long request is not left in thousands of parts. Every warp keeps its own ring of tiles full with
-// cp.async (waits are for its own copies only) and runs up to one stretch ahead of the one it works on. Parts of one
-// pair meet in the workspace; whoever brings the last one joins them, in order.
+// Work. Each CTA scans the lengths itself (no second launch, nothing on the host depends on them). With many (request,
+// KV head) pairs a worker is a warp: the pages of all pairs, in order, are dealt to the warps (Deal), so that a share
+// covers some pairs whole and one at either end in part; no barrier, nothing shared. With at most half as many pairs as
+// CTAs a worker is a CTA ("team"): a pair is cut into equal chunks of at most pages / (CTAs - pairs), no more than there
+// are CTAs, whose pages go round the warps by twos and whose sums meet in shared memory. Every warp keeps its own ring of
+// tiles full with cp.async (waits are for its own copies only) and runs up to one stretch ahead of the one it works on.
+// Parts of one pair meet in the workspace; a worker reports its parts, two at most, when its share is done, and whoever
+// brings the last one joins them, in order.
 template <int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attention_kernel(const __grid_constant__ Kv4AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid_constant__ Kv4AttnArgs a) {
     constexpr int NG = D / 32, NW = NG / 2;
     using S = Smem<D>;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     S& s = *reinterpret_cast<S*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-    // --- the batch: pages before each thread's requests, and the share of a worker
+    // --- the batch: how its pages are dealt, and the places before each thread's requests
     const int per = (a.R + kThreads - 1) / kThreads;
-    int64_t total;
+    const bool team = 2 * (int64_t)a.R * a.nkv <= gridDim.x;
+    const int workers = team ? gridDim.x : gridDim.x * kWarps;
+    const int worker = team ? blockIdx.x : blockIdx.x * kWarps + warp;
     {
         const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
+        Deal d;
+        d.chunk = 0;
         int keys;
-        int64_t sum = 0;
-        for (int r = r0; r < r1; ++r) sum += pages_of(a, r, &keys, blockIdx.x == 0);
-        const int64_t upto = warp_prefix(sum * a.nkv, lane);
-        if (lane == 31) s.scan[warp] = upto;
-        __syncthreads();
-        int64_t before = 0;
-        total = 0;
+        int64_t sum = 0, upto, before;
+        auto scan = [&]() {
+            upto = warp_prefix(sum * a.nkv, lane);
+            if (lane == 31) s.scan[warp] = upto;
+            __syncthreads();
+            before = d.total = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += s.scan[w];
-            total += s.scan[w];
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) before += s.scan[w];
+                d.total += s.scan[w];
+            }
+            __syncthreads();
+        };
+        if (team) {
+            for (int r = r0; r < r1; ++r) sum += pages_of(a, r, &keys, false);
+            scan();
+            const int64_t others = workers - a.R * a.nkv;
+            d.chunk = (int)min(max((d.total + others - 1) / others, (int64_t)(2 * kWarps)), (int64_t)0x7fffffff);
+            sum = 0;
         }
+        for (int r = r0; r < r1; ++r) sum += d.places(pages_of(a, r, &keys, blockIdx.x == 0));
+        scan();
+        d.share = team ? 1 : max((d.total + workers - 1) / workers, (int64_t)kMinShare);
         s.start[tid + 1] = before + upto;
-        if (tid == 0) s.start[0] = 0;
+        if (tid == 0) {
+            s.start[0] = 0;
+            s.deal = d;
+        }
         __syncthreads();
     }
     // requests without keys: zeros
@@ -368,87 +423,82 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attention_kernel(con
             for (int i = tid * 8; i < a.nkv * a.G * D; i += kThreads * 8)
                 *reinterpret_cast<uint4*>(a.out + r * a.out_stride + i) = make_uint4(0, 0, 0, 0);
     }
-    const bool team = 2 * (int64_t)a.R * a.nkv <= gridDim.x;
-    const int workers = team ? gridDim.x : gridDim.x * kWarps, worker = team ? blockIdx.x : blockIdx.x * kWarps + warp;
-    const int64_t share = max((total + workers - 1) / workers, (int64_t)kMinShare);
-    int64_t pos = worker * share;
-    const int64_t stop = min(total, pos + share);
+    int64_t pos = worker * s.deal.share;
+    const int64_t stop = min(s.deal.total, pos + s.deal.share);
 
     // --- this warp's stretches and its ring of tile pairs. Pair i is pages step i + offset and the next one.
     const int step = team ? 2 * kWarps : 2, offset = team ? 2 * warp : 0;
     int flying = 0;                // pairs on their way or waiting: cp.async groups in flight at most
     uint32_t absent = 0;           // two bits per stage: no such page, or one outside the pool
     int in_st = 0, out_st = 0;     // stages of the next pair issued, used
-    int ahead = 0, left = 0, at_pair = 0, ids = 0;  // items begun to load; pairs to come of the last of them
+    int ahead = 0;                 // stretches begun to load; of the last of them:
+    int rem = 0, head = 0;         // pages from the next pair on, its head
+    const int* idp = a.indices;    // their places in the page table
+    int id0 = -1, id1 = -1;        // the next pair's pages, fetched while the pair before is worked on
     const uint32_t my_ring = smem_u32(s.ring[warp]) + lane * 16;
     const uint8_t* const my_pool = a.pool + lane * 16;
-    auto fill = [&](int working) {  // `working`: the item that the warp works on
+    auto fetch_ids = [&]() {
+        id0 = rem > 0 ? __ldg(idp) : -1;
+        id1 = rem > 1 ? __ldg(idp + 1) : -1;
+    };
+    auto issue = [&]() {  // the next pair's tiles (rem > 0)
+        const bool bad0 = (unsigned)id0 >= (unsigned)a.num_pages, bad1 = (unsigned)id1 >= (unsigned)a.num_pages;
+        const uint32_t dst = my_ring + in_st * 2 * S::kHead;
+        const uint8_t* src0 = my_pool + ((int64_t)id0 * a.nkv + head) * S::kHead;
+        const uint8_t* src1 = my_pool + ((int64_t)id1 * a.nkv + head) * S::kHead - S::kHead;
+        constexpr int kPieces = (2 * S::kHead + 511) / 512;  // piece lane + 32 i of the two tiles, 16 bytes
+        absent &= ~(3u << 2 * in_st);
+        if (!bad0 && !bad1) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const bool second = 512 * i >= S::kHead || (512 * i + 512 > S::kHead && 512 * i + lane * 16 >= S::kHead);
+                if (512 * i + 512 <= 2 * S::kHead || 512 * i + lane * 16 < 2 * S::kHead)
+                    cp_async(dst + 512 * i, (second ? src1 : src0) + 512 * i);
+            }
+        } else {
+            if (bad0 || (bad1 && rem > 1)) set_status(a.status, NF_ERR_DEVICE_BOUNDS);
+            absent |= ((uint32_t)bad0 | (uint32_t)bad1 << 1) << 2 * in_st;
+#pragma unroll 1
+            for (int i = 0; i < kPieces; ++i) {
+                const int at = 512 * i + lane * 16;
+                if (at < S::kHead ? !bad0 : at < 2 * S::kHead && !bad1)
+                    cp_async(dst + 512 * i, (at < S::kHead ? src0 : src1) + 512 * i);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ++flying;
+        if (++in_st == kStages) in_st = 0;
+        rem -= step;
+        idp += step;
+        fetch_ids();
+    };
+    auto fill = [&](int working) {  // `working`: the stretch that the warp works on
         while (flying < kStages) {
-            if (left == 0) {
+            if (rem <= 0) {
                 if (pos >= stop || ahead > working + 1) return;
                 Item& it = s.item[warp][ahead & 1];
-                find_item<D>(a, s, pos, share, per, &it);
-                if (it.r < 0) {
-                    pos = stop;
-                    return;
-                }
-                pos += it.pages;
+                pos = find_item<D>(a, s, s.deal, pos, stop, worker, per, &it);
+                if (it.r < 0) continue;
                 ++ahead;
-                left = max(0, (it.pages - offset + step - 1) / step);
-                at_pair = 0;
-                if (left == 0) continue;
-                // q of the item, in one group with its first tiles
+                rem = it.pages - offset;
+                if (rem <= 0) continue;
+                head = it.h;
+                idp = a.indices + it.first + offset;
+                fetch_ids();
+                // q of the stretch, in one group with its first tiles
                 const uint8_t* q = reinterpret_cast<const uint8_t*>(a.q + it.r * a.q_stride + (int64_t)it.h * a.G * D);
                 const uint32_t dst = smem_u32(s.q[warp][(ahead - 1) & 1]);
                 for (int i = lane * 16; i < a.G * D * 2; i += 512) cp_async(dst + i, q + i);
             }
-            if ((at_pair & 15) == 0) {  // lane l: tile of the l-th page of the next 16 pairs; -1: none, or outside
-                const Item& it = s.item[warp][(ahead - 1) & 1];
-                const int p = step * (at_pair + (lane >> 1)) + offset + (lane & 1);
-                ids = -1;
-                if (p < it.pages) {
-                    const int page = __ldg(a.indices + it.first + p);
-                    if ((unsigned)page < (unsigned)a.num_pages)
-                        ids = page * a.nkv + it.h;
-                    else
-                        set_status(a.status, NF_ERR_DEVICE_BOUNDS);
-                }
-            }
-            const int t0 = __shfl_sync(0xffffffffu, ids, 2 * (at_pair & 15));
-            const int t1 = __shfl_sync(0xffffffffu, ids, 2 * (at_pair & 15) + 1);
-            const uint32_t dst = my_ring + in_st * 2 * S::kHead;
-            const uint8_t* src0 = my_pool + (int64_t)t0 * S::kHead;
-            const uint8_t* src1 = my_pool + (int64_t)t1 * S::kHead - S::kHead;
-            constexpr int kPieces = (2 * S::kHead + 511) / 512;  // piece lane + 32 i of the two tiles, 16 bytes
-            absent &= ~(3u << 2 * in_st);
-            if ((t0 | t1) >= 0) {
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const bool second = 512 * i >= S::kHead || (512 * i + 512 > S::kHead && 512 * i + lane * 16 >= S::kHead);
-                    if (512 * i + 512 <= 2 * S::kHead || 512 * i + lane * 16 < 2 * S::kHead)
-                        cp_async(dst + 512 * i, (second ? src1 : src0) + 512 * i);
-                }
-            } else {
-                absent |= ((uint32_t)(t0 < 0) | (uint32_t)(t1 < 0) << 1) << 2 * in_st;
-#pragma unroll 1
-                for (int i = 0; i < kPieces; ++i) {
-                    const int at = 512 * i + lane * 16;
-                    if (at < S::kHead ? t0 >= 0 : at < 2 * S::kHead && t1 >= 0)
-                        cp_async(dst + 512 * i, (at < S::kHead ? src0 : src1) + 512 * i);
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            ++flying;
-            ++at_pair;
-            --left;
-            if (++in_st == kStages) in_st = 0;
+            issue();
         }
     };
 
     const int gid = lane >> 2, tig = lane & 3;
     const uint32_t one = a.one;
+    int pending = 0;  // parts written, to be reported
     for (int k = 0;; ++k) {
-        fill(k);
+        if (flying < kStages) fill(k);
         if (k >= ahead) break;
         const int pages = s.item[warp][k & 1].pages, keys = s.item[warp][k & 1].keys;
         float O[NG][2][4], M0 = -INFINITY, M1 = -INFINITY, l0 = 0.f, l1 = 0.f;
@@ -531,6 +581,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attention_kernel(con
                 }
             }
             for (int p = offset; p < pages; p += step) {
+                if (flying < kStages) fill(k);  // (a new stretch to begin)
                 if (flying == kStages)
                     cp_async_wait<kStages - 1>();
                 else
@@ -696,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attention_kernel(con
                 __syncwarp();  // all read: the stage may be filled again
                 --flying;
                 if (++out_st == kStages) out_st = 0;
-                fill(k);
+                if (rem > 0) issue();
                 if (none != 3u) add_tile(y[1], ta[1], tb[1]);
             }
         }
@@ -707,64 +758,58 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attention_kernel(con
             l1 += __shfl_xor_sync(0xffffffffu, l1, o);
         }
         const Item it = s.item[warp][k & 1];
-        if (team) {
-            __syncthreads();  // the sums of the stretch before have been read
+        if (team) {  // (one stretch: the sums have their memory for themselves)
             if (gid == 0) {
                 s.ml[warp][2 * tig] = make_float2(M0, l0);
                 s.ml[warp][2 * tig + 1] = make_float2(M1, l1);
             }
         }
         const int64_t part = part_slot(it, it.c);
-#pragma unroll 1
-        for (int h0 = 0; h0 < a.G; h0 += S::kHeads) {
-            // rows of heads 2 t, 2 t + 1: columns 32 u + 4 g .. + 3
-            const int mine = 2 * tig - h0;
-            if (team && h0) __syncthreads();
-            if (mine >= 0 && mine < S::kHeads) {
+        // rows of heads 2 t, 2 t + 1: columns 32 u + 4 g .. + 3
 #pragma unroll
-                for (int u = 0; u < NG; ++u) {
-                    const uint32_t fu = u % 2 ? f[u / 2] >> 16 : f[u / 2] & 0xFFFFu;
-                    const float g = over_pow2(6, fu), ge = over_pow2(10, fu);
-                    const float4 o0 = make_float4(O[u][0][0] * ge, O[u][0][2] * g, O[u][1][0] * ge, O[u][1][2] * g);
-                    const float4 o1 = make_float4(O[u][0][1] * ge, O[u][0][3] * g, O[u][1][1] * ge, O[u][1][3] * g);
-                    const int col = 32 * u + 4 * gid;
-                    if (team) {
-                        *reinterpret_cast<float4*>(&s.merge[warp][mine][col]) = o0;
-                        *reinterpret_cast<float4*>(&s.merge[warp][mine + 1][col]) = o1;
-                    } else if (it.parts == 1) {
-                        if (2 * tig < a.G) store_out(a, it, D, 2 * tig, col, o0, l0);
-                        if (2 * tig + 1 < a.G) store_out(a, it, D, 2 * tig + 1, col, o1, l1);
-                    } else {
-                        float* po = a.part_o + (part * a.G + 2 * tig) * D + col;
-                        if (2 * tig < a.G) __stcg(reinterpret_cast<float4*>(po), o0);
-                        if (2 * tig + 1 < a.G) __stcg(reinterpret_cast<float4*>(po + D), o1);
-                    }
-                }
-            }
-            if (!team) continue;
-            __syncthreads();
-            const int col = tid % (D / 4) * 4, row = tid / (D / 4), h = h0 + row;
-            if (h >= a.G) continue;
-            float M = -INFINITY, L = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s.ml[w][h].x);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float2 ml = s.ml[w][h];
-                const float c = part_factor(ml.x, M);
-                const float4 v = *reinterpret_cast<const float4*>(&s.merge[w][row][col]);
-                L += c * ml.y;
-                o.x += c * v.x;
-                o.y += c * v.y;
-                o.z += c * v.z;
-                o.w += c * v.w;
-            }
-            if (it.parts == 1) {
-                store_out(a, it, D, h, col, o, L);
+        for (int u = 0; u < NG; ++u) {
+            const uint32_t fu = u % 2 ? f[u / 2] >> 16 : f[u / 2] & 0xFFFFu;
+            const float g = over_pow2(6, fu), ge = over_pow2(10, fu);
+            const float4 o0 = make_float4(O[u][0][0] * ge, O[u][0][2] * g, O[u][1][0] * ge, O[u][1][2] * g);
+            const float4 o1 = make_float4(O[u][0][1] * ge, O[u][0][3] * g, O[u][1][1] * ge, O[u][1][3] * g);
+            const int col = 32 * u + 4 * gid;
+            if (team) {
+                *reinterpret_cast<float4*>(&s.merge[warp][2 * tig][col]) = o0;
+                *reinterpret_cast<float4*>(&s.merge[warp][2 * tig + 1][col]) = o1;
+            } else if (it.parts == 1) {
+                if (2 * tig < a.G) store_out(a, it, D, 2 * tig, col, o0, l0);
+                if (2 * tig + 1 < a.G) store_out(a, it, D, 2 * tig + 1, col, o1, l1);
             } else {
-                __stcg(reinterpret_cast<float4*>(a.part_o + (part * a.G + h) * D + col), o);
-                if (col == 0) __stcg(a.part_ml + part * kMaxGroup + h, make_float2(M, L));
+                float* po = a.part_o + (part * a.G + 2 * tig) * D + col;
+                if (2 * tig < a.G) __stcg(reinterpret_cast<float4*>(po), o0);
+                if (2 * tig + 1 < a.G) __stcg(reinterpret_cast<float4*>(po + D), o1);
+            }
+        }
+        if (team) {
+            __syncthreads();
+            const int col = tid % (D / 4) * 4, h = tid / (D / 4);  // thread -> 4 columns of one head
+            if (h < a.G) {
+                float M = -INFINITY, L = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s.ml[w][h].x);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 ml = s.ml[w][h];
+                    const float c = part_factor(ml.x, M);
+                    const float4 v = *reinterpret_cast<const float4*>(&s.merge[w][h][col]);
+                    L += c * ml.y;
+                    o.x += c * v.x;
+                    o.y += c * v.y;
+                    o.z += c * v.z;
+                    o.w += c * v.w;
+                }
+                if (it.parts == 1) {
+                    store_out(a, it, D, h, col, o, L);
+                } else {
+                    __stcg(reinterpret_cast<float4*>(a.part_o + (part * a.G + h) * D + col), o);
+                    if (col == 0) __stcg(a.part_ml + part * kMaxGroup + h, make_float2(M, L));
+                }
             }
         }
         if (it.parts > 1) {
@@ -772,25 +817,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attention_kernel(con
                 __stcg(a.part_ml + part * kMaxGroup + 2 * tig, make_float2(M0, l0));
                 __stcg(a.part_ml + part * kMaxGroup + 2 * tig + 1, make_float2(M1, l1));
             }
-            __threadfence();
-            int last = 0;
-            if (team) __syncthreads(); else __syncwarp();
-            if (team ? tid == 0 : lane == 0) {
-                last = atomicAdd(a.arrived + it.slot, 1) == it.parts - 1;
-                if (last) a.arrived[it.slot] = 0;
-                if (team) s.last = last;
-            }
-            if (team) {
-                __syncthreads();
-                last = s.last;
-            } else {
-                last = __shfl_sync(0xffffffffu, last, 0);
-            }
-            if (last) {
-                __threadfence();
-                join_parts<D>(a, it, team ? warp : 0, team ? kWarps : 1);
-            }
+            if (lane == 0) s.pending[warp][pending] = it;
+            ++pending;
         }
+    }
+    if (pending) {  // (all warps of a team have the same)
+        __threadfence();
+        if (team) __syncthreads(); else __syncwarp();
+        int last = 0;
+        if ((team ? tid : lane) < pending) {
+            const Item& it = s.pending[warp][lane];
+            last = atomicAdd(a.arrived + it.slot, 1) == it.parts - 1;
+            if (last) a.arrived[it.slot] = 0;
+            if (team) s.last[lane] = last;
+        }
+        if (team) __syncthreads();
+        __threadfence();
+        for (int i = 0; i < pending; ++i)
+            if (team ? s.last[i] : __shfl_sync(0xffffffffu, last, i)) {
+                const Item& it = s.pending[warp][i];
+                if (team) {
+                    if (2 * warp < a.G) join_parts<D, 2>(a, it, 2 * warp);
+                } else {
+                    for (int h0 = 0; h0 < a.G; h0 += 4) join_parts<D, 4>(a, it, h0);
+                }
+            }
     }
 }
 
@@ -807,7 +858,7 @@ struct Workspace {
 
 template <int D>
 cudaError_t launch(const Kv4AttnArgs& a, int grid, cudaStream_t s) {
-    static_assert(kCtasPerSm * (sizeof(Smem<D>) + 1024) <= 228 * 1024, "CTAs of an SM share its memory");
+    static_assert(sizeof(Smem<D>) <= 227 * 1024, "shared memory of a CTA");
     const cudaError_t e = cudaFuncSetAttribute(kv4_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)sizeof(Smem<D>));
     if (e != cudaSuccess) return e;
@@ -858,7 +909,7 @@ extern "C" nf_status nf_op_kv4_decode_attention(const void* q, int64_t q_stride,
     int sms = nf::device_sm_count();
     if (sms <= 0) return NF_ERR_CUDA;
     if (sm_count > 0 && sm_count < sms) sms = sm_count;
-    const int grid = std::min(sms * nf::kCtasPerSm, nf::kMaxCtas);
+    const int grid = std::min(sms, nf::kMaxCtas);
     const double scale = softmax_scale > 0.f ? (double)softmax_scale : 1.0 / std::sqrt((double)head_dim);
     const int G = n_q_heads / n_kv_heads;
     const nf::Workspace at(G, head_dim);
