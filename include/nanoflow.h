@@ -578,7 +578,8 @@ int64_t nf_kv4_page_bytes(int32_t n_kv_heads, int32_t head_dim);
 /* Write num_tokens rows of K and V (k_dtype and v_dtype; [n_kv_heads x head_dim] each) to the slots of a 4-bit pool.
  * slots[t] = -1 skips the row; any other id outside the pool latches NF_ERR_DEVICE_BOUNDS and is
  * skipped. The slots of one call must differ (two rows written to one slot may leave a mixture of both).
- * Strides are multiples of 4 elements and k and v aligned to 4 elements, else NF_ERR_INVALID_ARGUMENT. */
+ * k, v and their row strides are multiples of 16 bytes and num_tokens * n_kv_heads is at most 2^30, else
+ * NF_ERR_INVALID_ARGUMENT. */
 nf_status nf_op_kv4_append(const void* k, int64_t k_stride, int32_t k_dtype, const void* v, int64_t v_stride,
                            int32_t v_dtype, const int32_t* slots, int32_t num_tokens, void* pool, int32_t num_pages,
                            int32_t n_kv_heads, int32_t head_dim, int32_t* status_device, void* stream);

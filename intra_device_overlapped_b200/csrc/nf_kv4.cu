@@ -11,6 +11,7 @@ namespace nf {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int kUnroll = 4;  // heads of a lane, in flight together
 constexpr float kLargest = 0x1p60f, kSmallest = 0x1p-60f;
 
 struct Kv4RowArgs {
@@ -21,135 +22,175 @@ struct Kv4RowArgs {
     int T, num_pages, nkv;
     uint8_t* pool;
     int* status;
+    FastDiv tasks;          // warps per token
 };
 
-// Work is dealt in lines: line 2 (t nkv + h) + w is head h of token t's K (w = 0) or V (w = 1) row, d / 4
-// lanes of 4 columns each. `lane4` is this lane's place in its line.
+// A warp takes kUnroll (D = 64: twice as many) heads of one token: D / 8 lanes a head's K row and the next D / 8 its V
+// row, 8 columns each. Lane m's codes (columns 8 m .. 8 m + 7, group m / 4) are one 4-byte word of a K tile and two 2-byte
+// units, d / 8 bytes apart, of a V tile. All that depends on the token is found once for all heads: with a line of work
+// for each (token, head) of its own the kernels were bound by address arithmetic (310 instructions a line).
 template <int D>
-struct Line {
-    int t, h, which, lane4;
-    __device__ __forceinline__ Line(int64_t line, int nkv) {
-        which = (int)(line & 1);
-        const int64_t th = line >> 1;
-        t = (int)(th / nkv);
-        h = (int)(th - (int64_t)t * nkv);
-        lane4 = threadIdx.x & (D / 4 - 1);
+struct Task {
+    static constexpr int kLanes = D / 8, kAtOnce = 32 / (2 * kLanes), kHeads = kUnroll * kAtOnce;
+    int t, h, which, m;  // token, the lane's first head (then every kAtOnce-th)
+    int scale;           // of the group, from the codes
+    uint8_t* codes;      // in head h's tile; null: no slot
+    __device__ __forceinline__ Task(const Kv4RowArgs& a) {
+        const uint32_t lane = threadIdx.x & 31, warp = blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32;
+        t = a.tasks(warp);
+        codes = nullptr;
+        if (t >= a.T) return;
+        h = (warp - t * a.tasks.d) * kHeads + lane / (2 * kLanes);
+        which = lane / kLanes & 1;
+        m = lane & (kLanes - 1);
+        const int id = __ldg(a.slots + t);
+        if (id < 0 || (id >> 4) >= a.num_pages) {
+            if (id != -1 && lane == 0) set_status(a.status, NF_ERR_DEVICE_BOUNDS);
+            return;
+        }
+        const int slot = id & 15;
+        const int at = which ? (slot >> 3) * 4 * D + ((slot & 7) >> 1) * D + 2 * (m & 3) * (D / 8) + 4 * (m >> 2) + 2 * (slot & 1)
+                             : slot * (D / 2) + (m & 3) * (D / 8) + 4 * (m >> 2);
+        scale = 8 * D + (slot * (D / 32) + (m >> 2)) * 2 - at;
+        codes = a.pool + ((int64_t)(id >> 4) * a.nkv + h) * (2 * kv4_tile_bytes(D)) + which * kv4_tile_bytes(D) + at;
     }
-    // where this lane's 4 codes stand in its tile: V, the 2-byte unit; K, the 4-byte word that lanes 2 i and
-    // 2 i + 1 share (p = 0, 1 and p = 2, 3: the low and the high byte of each half)
-    __device__ __forceinline__ int v_unit(int slot) const {
-        return (slot >> 3) * 4 * D + ((slot & 7) >> 1) * D + (lane4 & 7) * (D / 8) + 4 * (lane4 >> 3) + 2 * (slot & 1);
-    }
-    __device__ __forceinline__ int k_word(int slot) const {
-        return slot * (D / 2) + ((lane4 & 7) >> 1) * (D / 8) + 4 * (lane4 >> 3);
-    }
-    __device__ __forceinline__ int scale_at(int slot) const { return 8 * D + (slot * (D / 32) + (lane4 >> 3)) * 2; }
 };
 
-// Code of x in units of s: the exact quotient x / s rounded half to even. x * (1 / s) is off by under 2^-22 of
-// it, so k is the right integer or, next to a border, its neighbour; x - k s has at most 24 bits there
-// (|x - k s| <= s and x is no finer than 2^-24 s where k != 0), so the fma gives it exactly and tells the
-// side. |x| <= 7.04 s: no code leaves -7..7.
-__device__ __forceinline__ int code_of(float x, float s, float inv) {
-    float k = rintf(x * inv);
-    const float r = fmaf(-k, s, x), half = 0.5f * s;
-    const bool odd = ((int)k & 1) != 0;
-    if (fabsf(r) > half || (fabsf(r) == half && odd)) k += r > 0.f ? 1.f : -1.f;
-    return (int)k + 8;
+// Bits of 1.5 * 2^23 + k, k the code of x in units of s: the exact quotient x / s rounded half to even. The sum 1.5 *
+// 2^23 + x inv, inv within 2^-22 of 1 / s, rounds to an integer in its last bits (no conversion instruction: those run at
+// a quarter of the rate); it is the right one or, next to a border, its neighbour. x - k s has at most 24 bits there
+// (|x - k s| <= s and x is no finer than 2^-24 s where k != 0), so the fma gives it exactly: its double against s, the
+// tie going to even, tells. |x| <= 7.04 s: no code leaves -7..7.
+__device__ __forceinline__ int code_bits(float x, float s, float inv) {
+    constexpr float kMagic = 12582912.f;
+    const float t = fmaf(x, inv, kMagic), r = fmaf(kMagic - t, s, x);
+    int k = __float_as_int(t);
+    if (__float_as_int(fabsf(r) + fabsf(r)) + (k & 1) > __float_as_int(s)) k += 1 | (__float_as_int(r) >> 31);
+    return k;
 }
 
+// Nibble 2 p + h of a word to nibble p of half h, and back
+__device__ __forceinline__ uint32_t unshuffle_nibbles(uint32_t x) {
+    uint32_t t = (x ^ (x >> 4)) & 0x00F000F0u;
+    x ^= t ^ (t << 4);
+    t = (x ^ (x >> 8)) & 0x0000FF00u;
+    return x ^ t ^ (t << 8);
+}
+__device__ __forceinline__ uint32_t shuffle_nibbles(uint32_t x) {
+    uint32_t t = (x ^ (x >> 8)) & 0x0000FF00u;
+    x ^= t ^ (t << 8);
+    t = (x ^ (x >> 4)) & 0x00F000F0u;
+    return x ^ t ^ (t << 4);
+}
+
+// Append. A group's largest magnitude is found by 4 lanes, its scale by each of them; a K row's codes are written as 4-byte
+// words of 64 (32) consecutive bytes, a V row's as 2-byte units of 4 (2) sectors that two neighbouring slots share and L2
+// joins. All of a lane's rows are loaded before the first is quantised.
 template <int D, typename TK, typename TV>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowArgs a) {
-    constexpr int kPerBlock = kRowThreads / (D / 4);
-    const int64_t lines = (int64_t)a.T * a.nkv * 2;
-    // every lane of a warp stays in the loop (the shuffles need all of them)
-    for (int64_t base = (int64_t)blockIdx.x * kPerBlock; base < lines; base += (int64_t)gridDim.x * kPerBlock) {
-        const int64_t line = base + threadIdx.x / (D / 4);
-        const bool live = line < lines;
-        const Line<D> l(live ? line : 0, a.nkv);
-        const int slot_id = live ? __ldg(a.slots + l.t) : -1;
-        const bool ok = slot_id >= 0 && (slot_id >> 4) < a.num_pages;
-        if (!ok && slot_id != -1) set_status(a.status, NF_ERR_DEVICE_BOUNDS);
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ok) {
-            const int64_t col = l.h * D + 4 * l.lane4;
-            x = l.which ? load_row4<TV>(a.v, l.t * a.v_stride + col) : load_row4<TK>(a.k, l.t * a.k_stride + col);
-        }
-        // largest magnitude of the group by its bits: ordered like the values, NaN above infinity
-        uint32_t top = max(max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu),
-                           max(__float_as_uint(x.z) & 0x7fffffffu, __float_as_uint(x.w) & 0x7fffffffu));
+    using W = Task<D>;
+    const W w(a);
+    if (w.codes == nullptr) return;  // (the whole warp)
+    float x[kUnroll][8];
+    auto load = [&](const auto* row) {
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int i = 0; i < kUnroll; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+            if (w.h + i * W::kAtOnce < a.nkv) load_row8(row + i * W::kAtOnce * D, x[i]);
+        }
+    };
+    const int64_t col = (int64_t)w.h * D + 8 * w.m;
+    if constexpr (sizeof(TK) == sizeof(TV)) {
+        load(static_cast<const TK*>(w.which ? a.v : a.k) + w.t * (w.which ? a.v_stride : a.k_stride) + col);
+    } else if (w.which) {
+        load(static_cast<const TV*>(a.v) + w.t * a.v_stride + col);
+    } else {
+        load(static_cast<const TK*>(a.k) + w.t * a.k_stride + col);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+        // largest magnitude of the group by its bits: ordered like the values, NaN above infinity
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[i][e]) & 0x7fffffffu);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const float big = __uint_as_float(top);
         const float ab = big <= kLargest * 2.f ? bf2f(f2bf(big)) : big;
         uint16_t sbits = 0;
-        uint32_t codes = 0x8888;
+        uint32_t codes = 0x88888888u;  // code of column 8 m + e in nibble e
         if (!(ab <= kLargest)) {
             sbits = 0x7FC0;
         } else if (ab >= kSmallest) {
-            // two roundings to bf16 (of the magnitude and of its seventh): the scale is stored in 16 bits, and the
-            // codes are taken against the stored value
-            sbits = f2bf(__fdiv_rn(ab, 7.f));
-            const float s = bf2f(sbits), inv = __frcp_rn(s);
-            codes = code_of(x.x, s, inv) | code_of(x.y, s, inv) << 4 | code_of(x.z, s, inv) << 8 |
-                    code_of(x.w, s, inv) << 12;
+            // Two roundings to bf16 (of the magnitude and of its seventh): the scale is stored in 16 bits, and the codes
+            // are taken against the stored value. ab has 8 bits, so ab / 7 is at least 2^-11 of it away from every border
+            // of bf16 and a product with 1 / 7, 2^-23 off, rounds like the quotient.
+            sbits = f2bf(ab * (1.f / 7.f));
+            const float s = bf2f(sbits);
+            float inv;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+            // sum of 16^e (0x4B400000 + k_e) plus what makes it the sum of 16^e (8 + k_e), in 32 bits
+            codes = 0x88888888u - 0x4B400000u * 0x11111111u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) codes += (uint32_t)code_bits(x[i][e], s, inv) << (4 * e);
         }
-        // K: columns 4 m .. 4 m + 3 are (p, h) = (p0, 0), (p0, 1), (p0 + 1, 0), (p0 + 1, 1), p0 = 0 on even lanes
-        // and 2 on odd ones: bytes h = 0, 1 of p0, p0 + 1
-        const uint32_t b0 = (codes & 15u) | (codes >> 4 & 0xF0u), b1 = (codes >> 4 & 15u) | (codes >> 8 & 0xF0u);
-        const uint32_t mine = b0 | b1 << 16;
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-        if (!ok) continue;
-        const int slot = slot_id & 15;
-        uint8_t* tile = a.pool + ((int64_t)(slot_id >> 4) * a.nkv + l.h) * (2 * kv4_tile_bytes(D)) +
-                        l.which * kv4_tile_bytes(D);
-        if (l.which) {
-            *reinterpret_cast<uint16_t*>(tile + l.v_unit(slot)) = (uint16_t)codes;
-        } else if ((l.lane4 & 1) == 0) {
-            *reinterpret_cast<uint32_t*>(tile + l.k_word(slot)) = mine | other << 8;
+        if (w.h + i * W::kAtOnce >= a.nkv) continue;
+        uint8_t* at = w.codes + i * W::kAtOnce * 2 * kv4_tile_bytes(D);
+        if (w.which) {
+            *reinterpret_cast<uint16_t*>(at) = (uint16_t)codes;
+            *reinterpret_cast<uint16_t*>(at + D / 8) = (uint16_t)(codes >> 16);
+        } else {
+            *reinterpret_cast<uint32_t*>(at) = unshuffle_nibbles(codes);
         }
-        if ((l.lane4 & 7) == 0) *reinterpret_cast<uint16_t*>(tile + l.scale_at(slot)) = sbits;
+        if ((w.m & 3) == 0) *reinterpret_cast<uint16_t*>(at + w.scale) = sbits;
     }
 }
 
+// Read: the reverse. Bound by the rows written.
 template <int D, typename T>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4RowArgs a) {
-    constexpr int kPerBlock = kRowThreads / (D / 4);
-    const int64_t lines = (int64_t)a.T * a.nkv * 2;
-    for (int64_t line = (int64_t)blockIdx.x * kPerBlock + threadIdx.x / (D / 4); line < lines;
-         line += (int64_t)gridDim.x * kPerBlock) {
-        const Line<D> l(line, a.nkv);
-        const int slot_id = __ldg(a.slots + l.t);
-        if (slot_id < 0 || (slot_id >> 4) >= a.num_pages) {
-            if (slot_id != -1) set_status(a.status, NF_ERR_DEVICE_BOUNDS);
-            continue;
-        }
-        const int slot = slot_id & 15;
-        const uint8_t* tile = a.pool + ((int64_t)(slot_id >> 4) * a.nkv + l.h) * (2 * kv4_tile_bytes(D)) +
-                              l.which * kv4_tile_bytes(D);
-        uint32_t codes;
-        if (l.which) {
-            codes = *reinterpret_cast<const uint16_t*>(tile + l.v_unit(slot));
+    using W = Task<D>;
+    const W w(a);
+    if (w.codes == nullptr) return;
+    uint32_t codes[kUnroll];
+    uint16_t scale[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+        if (w.h + i * W::kAtOnce >= a.nkv) continue;
+        const uint8_t* at = w.codes + i * W::kAtOnce * 2 * kv4_tile_bytes(D);
+        if (w.which) {
+            const uint32_t lo = *reinterpret_cast<const uint16_t*>(at);
+            codes[i] = lo | *reinterpret_cast<const uint16_t*>(at + D / 8) << 16;
         } else {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + l.k_word(slot)) >> ((l.lane4 & 1) * 8);
-            codes = (w & 15u) | (w >> 16 & 15u) << 4 | (w >> 4 & 15u) << 8 | (w >> 20 & 15u) << 12;
+            codes[i] = shuffle_nibbles(*reinterpret_cast<const uint32_t*>(at));
         }
-        const float s = bf2f(*reinterpret_cast<const uint16_t*>(tile + l.scale_at(slot)));
-        auto value = [&](int i) { return s * (float)((int)(codes >> (4 * i) & 15u) - 8); };
-        const int64_t at = (int64_t)l.t * (l.which ? a.v_stride : a.k_stride) + l.h * D + 4 * l.lane4;
-        store_row4<T>(l.which ? a.v_out : a.k_out, at, make_float4(value(0), value(1), value(2), value(3)));
+        scale[i] = *reinterpret_cast<const uint16_t*>(at + w.scale);
+    }
+    T* out = static_cast<T*>(w.which ? a.v_out : a.k_out) + w.t * (w.which ? a.v_stride : a.k_stride) + (int64_t)w.h * D +
+             8 * w.m;
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+        if (w.h + i * W::kAtOnce >= a.nkv) continue;
+        const float s = bf2f(scale[i]), bias = -8388616.f;
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)  // the code under the exponent of 2^23 (no conversion instruction)
+            x[e] = s * (__uint_as_float((codes[i] >> (4 * e) & 15u) | 0x4B000000u) + bias);
+        store_row8(out + i * W::kAtOnce * D, x);
     }
 }
 
+// Blocks of a launch, and its warps per token
 template <int D>
-int row_grid(const Kv4RowArgs& a) {
-    constexpr int kPerBlock = kRowThreads / (D / 4);
-    const int64_t blocks = ((int64_t)a.T * a.nkv * 2 + kPerBlock - 1) / kPerBlock;
-    return (int)(blocks < 148 * 8 ? blocks : 148 * 8);
+int row_grid(Kv4RowArgs& a) {
+    a.tasks = FastDiv((a.nkv + Task<D>::kHeads - 1) / Task<D>::kHeads);
+    return (int)(((int64_t)a.T * a.tasks.d + kRowThreads / 32 - 1) / (kRowThreads / 32));
 }
 
 template <int D>
-cudaError_t launch_append(const Kv4RowArgs& a, bool k32, bool v32, cudaStream_t s) {
+cudaError_t launch_append(Kv4RowArgs a, bool k32, bool v32, cudaStream_t s) {
     const int grid = row_grid<D>(a);
     if (k32)
         v32 ? kv4_append_kernel<D, float, float><<<grid, kRowThreads, 0, s>>>(a)
@@ -161,7 +202,7 @@ cudaError_t launch_append(const Kv4RowArgs& a, bool k32, bool v32, cudaStream_t 
 }
 
 template <int D>
-cudaError_t launch_read(const Kv4RowArgs& a, bool out32, cudaStream_t s) {
+cudaError_t launch_read(Kv4RowArgs a, bool out32, cudaStream_t s) {
     const int grid = row_grid<D>(a);
     out32 ? kv4_read_kernel<D, float><<<grid, kRowThreads, 0, s>>>(a)
           : kv4_read_kernel<D, uint16_t><<<grid, kRowThreads, 0, s>>>(a);
@@ -176,10 +217,11 @@ nf_status check_rows(const Kv4RowArgs& a, const void* k, const void* v, int32_t 
     const nf_status st = kv4_check_heads(a.nkv, d);
     if (st != NF_OK) return st;
     const int64_t row = (int64_t)a.nkv * d;
-    if (a.k_stride < row || a.v_stride < row || a.k_stride % 4 || a.v_stride % 4) return NF_ERR_INVALID_ARGUMENT;
-    if (!aligned(k, k_dtype == NF_DTYPE_F32 ? 16 : 8) || !aligned(v, v_dtype == NF_DTYPE_F32 ? 16 : 8) ||
-        !aligned(a.pool, 16))
-        return NF_ERR_INVALID_ARGUMENT;
+    const int k_unit = k_dtype == NF_DTYPE_F32 ? 4 : 8, v_unit = v_dtype == NF_DTYPE_F32 ? 4 : 8;  // 16 bytes
+    if (a.k_stride < row || a.v_stride < row || a.k_stride % k_unit || a.v_stride % v_unit) return NF_ERR_INVALID_ARGUMENT;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(a.pool, 16)) return NF_ERR_INVALID_ARGUMENT;
+    // (warps are counted in 32 bits)
+    if ((int64_t)a.T * a.nkv > 0x40000000) return NF_ERR_INVALID_ARGUMENT;
     if (a.T == 0) return NF_OK;
     return check_on_device(k, v, (const void*)a.slots, (const void*)a.pool, (const void*)a.status);
 }
@@ -197,7 +239,7 @@ extern "C" nf_status nf_op_kv4_append(const void* k, int64_t k_stride, int32_t k
                                       void* pool, int32_t num_pages, int32_t n_kv_heads, int32_t head_dim,
                                       int32_t* status_device, void* stream) try {
     const nf::Kv4RowArgs a{k, v, nullptr, nullptr, k_stride, v_stride, slots, num_tokens, num_pages, n_kv_heads,
-                           static_cast<uint8_t*>(pool), status_device};
+                           static_cast<uint8_t*>(pool), status_device, nf::FastDiv()};
     const nf_status st = nf::check_rows(a, k, v, head_dim, k_dtype, v_dtype);
     if (st != NF_OK || num_tokens == 0) return st;
     const bool k32 = k_dtype == NF_DTYPE_F32, v32 = v_dtype == NF_DTYPE_F32;
@@ -213,7 +255,8 @@ extern "C" nf_status nf_op_kv4_read(const void* pool, int32_t num_pages, const i
                                     int32_t n_kv_heads, int32_t head_dim, void* k_out, int64_t k_stride, void* v_out,
                                     int64_t v_stride, int32_t out_dtype, int32_t* status_device, void* stream) try {
     const nf::Kv4RowArgs a{nullptr, nullptr, k_out, v_out, k_stride, v_stride, slots, num_tokens, num_pages, n_kv_heads,
-                           static_cast<uint8_t*>(const_cast<void*>(pool)), status_device};
+                           static_cast<uint8_t*>(const_cast<void*>(pool)), status_device,
+                           nf::FastDiv()};
     const nf_status st = nf::check_rows(a, k_out, v_out, head_dim, out_dtype, out_dtype);
     if (st != NF_OK || num_tokens == 0) return st;
     const bool out32 = out_dtype == NF_DTYPE_F32;

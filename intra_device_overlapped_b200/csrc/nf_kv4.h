@@ -52,6 +52,48 @@ nf_status check_on_device(const P*... ptrs) {
     return NF_OK;
 }
 
+// n / d for 0 <= n < 2^31 and a divisor known on the host: with m = ceil(2^(31 + s) / d), 2^(s - 1) < d <= 2^s, the
+// error of n m / 2^(31 + s) is below n / 2^31 / d, too little to reach the next integer.
+struct FastDiv {
+    uint32_t m, s, d;
+    explicit FastDiv(uint32_t div = 1) : m(0), s(0), d(div) {
+        while ((1u << s) < div) ++s;
+        m = (uint32_t)(((uint64_t)(1ull << (31 + s)) + div - 1) / div);
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+        return (uint32_t)(((uint64_t)n * m) >> (31 + s));
+    }
+};
+
+// Eight consecutive values of a bf16 or fp32 row as fp32, and back (16 and 32 bytes, 16-byte aligned).
+template <typename T>
+__device__ __forceinline__ void load_row8(const T* row, float* x) {
+    if constexpr (sizeof(T) == 4) {
+        const float4 a = __ldcs(reinterpret_cast<const float4*>(row)), b = __ldcs(reinterpret_cast<const float4*>(row) + 1);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+        const uint4 w = __ldcs(reinterpret_cast<const uint4*>(row));
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(v[i] << 16);
+            x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_row8(T* row, const float* x) {
+    if constexpr (sizeof(T) == 4) {
+        reinterpret_cast<float4*>(row)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4*>(row)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        *reinterpret_cast<uint4*>(row) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                    pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    }
+}
+
 // Four consecutive values of a bf16 or fp32 row as fp32.
 template <typename T>
 __device__ __forceinline__ float4 load_row4(const void* row, int64_t at) {

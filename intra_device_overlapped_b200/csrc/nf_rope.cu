@@ -30,20 +30,85 @@ struct RopeArgs {
     int copy;  // columns behind `rot` have to be written (the output is another buffer or type)
 };
 
+// Cosines and sines of token t's positions, times `scale`, by `threads` threads.
+__device__ __forceinline__ void form_turns(const RopeArgs& a, int t, float2* cs, int thread, int threads) {
+    const double pos = (double)a.positions[t];
+    for (int i = thread; i < a.rot / 2; i += threads) {
+        // turns in 64 bits (131072 positions leave fp32 no bits of the fraction), then sin and cos of pi x
+        const double turn = pos * a.freq[i] * 0.15915494309189533577;
+        float s, c;
+        sincospif((float)(2.0 * (turn - rint(turn))), &s, &c);
+        cs[i] = make_float2(c * a.scale, s * a.scale);
+    }
+}
+
+// (x, y) at angle p f: (x c - y s, y c + x s). A token's turns are formed once, in shared memory, for all its heads; a
+// thread then takes 8 pairs of a head, two vectors of 8 columns in (16 bytes in bf16) and out. Every value is read and
+// written once, so the kernel is bound by HBM; kTokens tokens a block where there are enough of them keep all threads
+// busy with turns.
+template <typename TI, typename TO, int kTokens>
+__global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const RopeArgs a, const FastDiv per_token,
+                                                                const FastDiv per_head) {
+    __shared__ float2 cs[kTokens][kRopeMaxDim / 2];
+    const int t0 = blockIdx.x * kTokens, tokens = min(kTokens, a.T - t0), half = a.rot / 2;
+    constexpr int kShare = kRopeThreads / kTokens;
+    if ((int)threadIdx.x / kShare < tokens)
+        form_turns(a, t0 + threadIdx.x / kShare, cs[threadIdx.x / kShare], threadIdx.x % kShare, kShare);
+    __syncthreads();
+    const int units = tokens * per_token.d, turned = a.rot / 16;
+#pragma unroll 2
+    for (int e = threadIdx.x; e < units; e += kRopeThreads) {
+        const int tt = per_token(e), r = e - tt * per_token.d;
+        int h = per_head(r);
+        const int u = r - h * per_head.d;
+        const bool isq = h < a.q.heads;
+        const RopeSide& side = isq ? a.q : a.k;
+        h -= isq ? 0 : a.q.heads;
+        // columns i .. i + 7 and j .. j + 7
+        int i = 16 * u, j = i + 8;
+        if (u < turned && !a.interleaved) {
+            i = 8 * u;
+            j = i + half;
+        }
+        if (u >= turned && !a.copy) continue;
+        const TI* x = static_cast<const TI*>(side.in) + (t0 + tt) * side.in_stride + (int64_t)h * a.d;
+        TO* y = static_cast<TO*>(side.out) + (t0 + tt) * side.out_stride + (int64_t)h * a.d;
+        float p[8], q[8];
+        load_row8(x + i, p);
+        load_row8(x + j, q);
+        if (u < turned) {
+            if (a.interleaved) {
+#pragma unroll
+                for (int n = 0; n < 8; n += 2) {
+                    const float2 w = cs[tt][8 * u + n / 2], z = cs[tt][8 * u + 4 + n / 2];
+                    const float p0 = p[n], q0 = q[n];
+                    p[n] = p0 * w.x - p[n + 1] * w.y;
+                    p[n + 1] = p[n + 1] * w.x + p0 * w.y;
+                    q[n] = q0 * z.x - q[n + 1] * z.y;
+                    q[n + 1] = q[n + 1] * z.x + q0 * z.y;
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const float2 w = cs[tt][8 * u + n];
+                    const float p0 = p[n];
+                    p[n] = p0 * w.x - q[n] * w.y;
+                    q[n] = q[n] * w.x + p0 * w.y;
+                }
+            }
+        }
+        store_row8(y + i, p);
+        store_row8(y + j, q);
+    }
+}
+
 // One pair per step, any sizes and alignment.
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     __shared__ float2 cs[kRopeMaxDim / 2];
     const int half = a.rot / 2;
     for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const double pos = (double)a.positions[t];
-        for (int i = threadIdx.x; i < half; i += kRopeThreads) {
-            // turns in 64 bits (131072 positions leave fp32 no bits of the fraction), then sin and cos of pi x
-            const double turn = pos * a.freq[i] * 0.15915494309189533577;
-            float s, c;
-            sincospif((float)(2.0 * (turn - rint(turn))), &s, &c);
-            cs[i] = make_float2(c * a.scale, s * a.scale);
-        }
+        form_turns(a, t, cs, threadIdx.x, kRopeThreads);
         __syncthreads();
         const int units = a.d / 2, heads = a.q.heads + a.k.heads;
         for (int e = threadIdx.x; e < heads * units; e += kRopeThreads) {
@@ -76,9 +141,24 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
 }
 
 template <typename TI, typename TO>
+bool side_vec(const RopeSide& s) {
+    return s.heads == 0 || (aligned(s.in, 16) && aligned(s.out, 16) && s.in_stride * sizeof(TI) % 16 == 0 &&
+                            s.out_stride * sizeof(TO) % 16 == 0);
+}
+
+template <typename TI, typename TO>
 cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
-    const int grid = a.T < 148 * 8 ? a.T : 148 * 8;
-    rope_kernel<TI, TO><<<grid, kRopeThreads, 0, s>>>(a);
+    const int heads = a.q.heads + a.k.heads;
+    if (a.d % 16 == 0 && a.rot % 16 == 0 && side_vec<TI, TO>(a.q) && side_vec<TI, TO>(a.k)) {
+        const FastDiv per_token(heads * (a.d / 16)), per_head(a.d / 16);
+        if (a.T < 4096)
+            rope_vec_kernel<TI, TO, 1><<<a.T, kRopeThreads, 0, s>>>(a, per_token, per_head);
+        else
+            rope_vec_kernel<TI, TO, 4><<<(a.T + 3) / 4, kRopeThreads, 0, s>>>(a, per_token, per_head);
+    } else {
+        const int grid = a.T < 148 * 8 ? a.T : 148 * 8;
+        rope_kernel<TI, TO><<<grid, kRopeThreads, 0, s>>>(a);
+    }
     return cudaGetLastError();
 }
 

@@ -307,7 +307,7 @@ def test_read(nf, T, nkv, d, dt):
     if T > 8:
         slots[5] = -1
     pool, status = _dev(p.raw.reshape(-1)), _status()
-    kd = torch.full((T, nkv * d + 4), 9.0, dtype=TORCH[dt], device=DEV)
+    kd = torch.full((T, nkv * d + 8), 9.0, dtype=TORCH[dt], device=DEV)
     vd = torch.full((T, nkv * d), 9.0, dtype=TORCH[dt], device=DEV)
     sl = _i32(slots)
     nf.check(nf.nf_op_kv4_read(pool.data_ptr(), pages, sl.data_ptr(), T, nkv, d, kd.data_ptr(), kd.stride(0),

@@ -78,7 +78,7 @@ def test_rope_refusals(kw, want):
     (dict(T=-1), BAD), (dict(pages=0), BAD), (dict(pages=nf.NF_KV4_MAX_PAGES + 1), BAD), (dict(dt=2, vdt=2), BAD),
     (dict(nkv=0), BAD), (dict(d=0), BAD), (dict(d=96), UNSUP), (dict(nkv=257, ks=1 << 20, vs=1 << 20), UNSUP),
     (dict(ks=252), BAD), (dict(vs=258), BAD), (dict(k=P + 4), BAD), (dict(v=P + 8, dt=1, vdt=1), BAD), (dict(pool=P + 8), BAD),
-    (dict(T=0), 0)])
+    (dict(ks=260), BAD), (dict(T=1 << 30), BAD), (dict(T=0), 0)])
 def test_row_refusals(read, kw, want):
     assert _append(read, **kw) == want
 
