@@ -33,40 +33,61 @@ template <int D>
 struct Task {
     static constexpr int kLanes = D / 8, kAtOnce = 32 / (2 * kLanes), kHeads = kUnroll * kAtOnce;
     int t, h, which, m;  // token, the lane's first head (then every kAtOnce-th)
+    int id;              // the token's slot
     int scale;           // of the group, from the codes
-    uint8_t* codes;      // in head h's tile; null: no slot
+    uint8_t* codes;      // in head h's tile
     __device__ __forceinline__ Task(const Kv4RowArgs& a) {
         const uint32_t lane = threadIdx.x & 31, warp = blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32;
         t = a.tasks(warp);
-        codes = nullptr;
-        if (t >= a.T) return;
         h = (warp - t * a.tasks.d) * kHeads + lane / (2 * kLanes);
         which = lane / kLanes & 1;
         m = lane & (kLanes - 1);
-        const int id = __ldg(a.slots + t);
+        id = t < a.T ? __ldg(a.slots + t) : -1;
+    }
+    // false (for the whole warp): the token has no slot
+    __device__ __forceinline__ bool find(const Kv4RowArgs& a) {
         if (id < 0 || (id >> 4) >= a.num_pages) {
-            if (id != -1 && lane == 0) set_status(a.status, NF_ERR_DEVICE_BOUNDS);
-            return;
+            if (id != -1 && (threadIdx.x & 31) == 0) set_status(a.status, NF_ERR_DEVICE_BOUNDS);
+            return false;
         }
         const int slot = id & 15;
         const int at = which ? (slot >> 3) * 4 * D + ((slot & 7) >> 1) * D + 2 * (m & 3) * (D / 8) + 4 * (m >> 2) + 2 * (slot & 1)
                              : slot * (D / 2) + (m & 3) * (D / 8) + 4 * (m >> 2);
         scale = 8 * D + (slot * (D / 32) + (m >> 2)) * 2 - at;
         codes = a.pool + ((int64_t)(id >> 4) * a.nkv + h) * (2 * kv4_tile_bytes(D)) + which * kv4_tile_bytes(D) + at;
+        return true;
     }
 };
 
-// Bits of 1.5 * 2^23 + k, k the code of x in units of s: the exact quotient x / s rounded half to even. The sum 1.5 *
-// 2^23 + x inv, inv within 2^-22 of 1 / s, rounds to an integer in its last bits (no conversion instruction: those run at
-// a quarter of the rate); it is the right one or, next to a border, its neighbour. x - k s has at most 24 bits there
-// (|x - k s| <= s and x is no finer than 2^-24 s where k != 0), so the fma gives it exactly: its double against s, the
-// tie going to even, tells. |x| <= 7.04 s: no code leaves -7..7.
-__device__ __forceinline__ int code_bits(float x, float s, float inv) {
+// Codes of 8 values in units of s, code + 8 of x[e] in nibble e: the exact quotients x / s rounded half to even.
+// 1.5 * 2^23 + x inv, inv within 2^-22 of 1 / s, rounds to an integer k in its last bits (no conversion instruction:
+// those run at a quarter of the rate); it is the right one or, next to a border, its neighbour. The remainder x - k s has
+// at most 24 bits there (|x - k s| <= s and x is no finer than 2^-24 s where k != 0), so the fma gives it exactly: a
+// magnitude below s / 2 is settled, and else (in one of twenty warps) its double against s, the tie going to even,
+// tells. |x| <= 7.04 s: no code leaves -7..7.
+__device__ __forceinline__ uint32_t codes_of(const float* x, float s, float inv) {
     constexpr float kMagic = 12582912.f;
-    const float t = fmaf(x, inv, kMagic), r = fmaf(kMagic - t, s, x);
-    int k = __float_as_int(t);
-    if (__float_as_int(fabsf(r) + fabsf(r)) + (k & 1) > __float_as_int(s)) k += 1 | (__float_as_int(r) >> 31);
-    return k;
+    // the sum of 16^e (0x4B400000 + k_e), and what makes it the sum of 16^e (8 + k_e), in 32 bits
+    constexpr uint32_t kStart = 0x88888888u - 0x4B400000u * 0x11111111u;
+    uint32_t codes = kStart;
+    float worst = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float t = fmaf(x[e], inv, kMagic);
+        worst = fmaxf(worst, fabsf(fmaf(kMagic - t, s, x[e])));
+        codes += __float_as_uint(t) << (4 * e);
+    }
+    if (worst + worst >= s) {
+        codes = kStart;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float t = fmaf(x[e], inv, kMagic), r = fmaf(kMagic - t, s, x[e]);
+            int k = __float_as_int(t);
+            if (__float_as_int(fabsf(r) + fabsf(r)) + (k & 1) > __float_as_int(s)) k += 1 | (__float_as_int(r) >> 31);
+            codes += (uint32_t)k << (4 * e);
+        }
+    }
+    return codes;
 }
 
 // Nibble 2 p + h of a word to nibble p of half h, and back
@@ -85,12 +106,12 @@ __device__ __forceinline__ uint32_t shuffle_nibbles(uint32_t x) {
 
 // Append. A group's largest magnitude is found by 4 lanes, its scale by each of them; a K row's codes are written as 4-byte
 // words of 64 (32) consecutive bytes, a V row's as 2-byte units of 4 (2) sectors that two neighbouring slots share and L2
-// joins. All of a lane's rows are loaded before the first is quantised.
+// joins. All of a lane's rows are loaded before the first is quantised, and before its token's slot is known.
 template <int D, typename TK, typename TV>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowArgs a) {
     using W = Task<D>;
-    const W w(a);
-    if (w.codes == nullptr) return;  // (the whole warp)
+    W w(a);
+    if (w.t >= a.T) return;
     float x[kUnroll][8];
     auto load = [&](const auto* row) {
 #pragma unroll
@@ -108,6 +129,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowArg
     } else {
         load(static_cast<const TK*>(a.k) + w.t * a.k_stride + col);
     }
+    if (!w.find(a)) return;
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
@@ -131,10 +153,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowArg
             const float s = bf2f(sbits);
             float inv;
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-            // sum of 16^e (0x4B400000 + k_e) plus what makes it the sum of 16^e (8 + k_e), in 32 bits
-            codes = 0x88888888u - 0x4B400000u * 0x11111111u;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) codes += (uint32_t)code_bits(x[i][e], s, inv) << (4 * e);
+            codes = codes_of(x[i], s, inv);
         }
         if (w.h + i * W::kAtOnce >= a.nkv) continue;
         uint8_t* at = w.codes + i * W::kAtOnce * 2 * kv4_tile_bytes(D);
@@ -152,8 +171,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowArg
 template <int D, typename T>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4RowArgs a) {
     using W = Task<D>;
-    const W w(a);
-    if (w.codes == nullptr) return;
+    W w(a);
+    if (!w.find(a)) return;
     uint32_t codes[kUnroll];
     uint16_t scale[kUnroll];
 #pragma unroll
