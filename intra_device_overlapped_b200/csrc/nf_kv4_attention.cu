@@ -19,8 +19,8 @@ constexpr int kWarps = 12;                 // one CTA per SM, 168 registers a th
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;                 // pairs of tiles in flight per warp
 constexpr int kMaxCtas = 160;              // sizes the workspace (a B200 has 148 SMs)
-constexpr int kMinShare = 16;              // pages of a worker at least
-constexpr int kOverhead = 6;               // what beginning and ending a (request, head) costs, in pages
+constexpr int kMinShare = 4;               // places of a worker at least (Deal)
+constexpr int kOverhead = 10;              // what beginning and ending a (request, head) costs, in pages
 constexpr int kMaxParts = 2 * kWarps * kMaxCtas;
 
 struct Kv4AttnArgs {
