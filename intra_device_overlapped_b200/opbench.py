@@ -8,7 +8,9 @@ paged pool), ``prefill_attention`` (the workload's prefill chunk), ``gemm`` (--m
 random operands), ``iteration`` (whole serving iterations of the workload with a plan forced by
 --nano / --template / --sm-attn, the sequential one by default; one iteration of the Llama-3-8B
 layer launches the QKV, O, gate/up and down GEMMs in that order; --persistent runs each layer as
-one persistent kernel instead). ``--sm`` is the persistent grid (0 = every SM). The printed line holds the mean
+one persistent kernel instead), and on the workload's decode batch, over a 4-bit KV cache of one layer,
+``kv4_decode_attention`` and the operations that feed it: ``page_map``, ``rope``, ``kv4_append`` and
+``kv4_read`` (the last two on --rows rows in place of the batch's, if given). ``--sm`` is the persistent grid (0 = every SM). The printed line holds the mean
 launch time over --reps launches (CUDA events on the launching stream, after --warmup launches) and
 the algorithmic bytes or FLOPs of one launch, so that a profiler can target a small, known case.
 --power-s S adds the op's steady state under load: S seconds of back-to-back launches after 1 s,
@@ -22,7 +24,11 @@ import json
 import numpy as np
 import torch
 
-from . import check, nf_op_decode_attention, nf_op_gemm_bf16, nf_op_prefill_attention
+from . import (NF_DTYPE_BF16, NF_DTYPE_F32, check, nf_kv4_page_bytes, nf_kv4_workspace_bytes, nf_op_decode_attention,
+               nf_op_gemm_bf16, nf_op_kv4_append, nf_op_kv4_decode_attention, nf_op_kv4_read, nf_op_page_map,
+               nf_op_prefill_attention, nf_op_rope, nf_rope_config, nf_rope_frequencies)
+
+KV4_OPS = ("kv4_decode_attention", "kv4_append", "kv4_read", "rope", "page_map")
 
 
 def _power(launch, seconds: float, stream) -> dict:
@@ -78,9 +84,77 @@ def _time(launch, reps: int, warmup: int, stream) -> float:
     return e0.elapsed_time(e1) * 1000.0 / reps
 
 
+def _kv4(args, w, dev, stream):
+    """One operation over a 4-bit cache of one layer of workload `w`: (launch, figures, bytes of one launch, status word)."""
+    from synth.workloads import make_batch
+    s, b = w.shape, make_batch(w)
+    R = args.requests or b.num_decode
+    nq, nkv, d = s.n_q_heads, s.n_kv_heads, s.head_dim
+    g = torch.Generator(device=dev).manual_seed(0)
+    i32 = lambda a: torch.as_tensor(np.ascontiguousarray(a, dtype=np.int32), device=dev)  # noqa: E731
+    randn = lambda *n: torch.randn(n, device=dev, generator=g)  # noqa: E731
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    ctx, st = np.asarray(b.ctx_lens[:R]), stream.cuda_stream
+    pages = -(-(ctx + 1) // s.page_size)
+    num_pages = int(b.num_pages)
+    if args.op == "page_map":
+        held = -(-ctx // s.page_size)
+        width = int(pages.max())
+        table = np.zeros((R, width))
+        for r in range(R):
+            table[r, :held[r]] = b.page_indices[b.page_indptr[r]:b.page_indptr[r] + held[r]]
+        spare = i32(np.concatenate([b.page_indices[b.page_indptr[r] + held[r]:b.page_indptr[r + 1]] for r in range(R)] +
+                                   [np.zeros(1)]))
+        lens, table, count, left = i32(ctx), i32(table), i32([spare.numel()]), i32([0])
+        out = [torch.empty(n, dtype=torch.int32, device=dev) for n in (R, R + 1, int(pages.sum()), R, R)]
+        launch = lambda: check(nf_op_page_map(  # noqa: E731
+            lens.data_ptr(), 0, R, table.data_ptr(), width, spare.data_ptr(), spare.numel(), count.data_ptr(), num_pages,
+            out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[2].numel(), out[3].data_ptr(), out[4].data_ptr(),
+            R, left.data_ptr(), status.data_ptr(), st), "page_map")
+        return launch, {"requests": R, "pages": int(pages.sum())}, 8 * int(pages.sum()) + 24 * R, status
+    if args.op == "rope":
+        T = args.rows or R
+        rows, pos = randn(T, (nq + 2 * nkv) * d), i32(np.resize(ctx, T))
+        code, freq, scale = nf_rope_frequencies(nf_rope_config(theta=s.rope_theta, rot_dim=d))
+        check(code, "rope frequencies")
+        freq = torch.tensor(freq, dtype=torch.float64, device=dev)
+        q, k = (torch.empty((T, n, d), dtype=torch.bfloat16, device=dev) for n in (nq, nkv))
+        launch = lambda: check(nf_op_rope(  # noqa: E731
+            rows.data_ptr(), rows.stride(0), q.data_ptr(), nq * d, nq, rows.data_ptr() + 4 * nq * d, rows.stride(0),
+            k.data_ptr(), nkv * d, nkv, NF_DTYPE_F32, NF_DTYPE_BF16, pos.data_ptr(), T, d, d, 0, freq.data_ptr(), scale,
+            st), "rope")
+        return launch, {"rows": T}, T * (nq + nkv) * d * 6, status
+    pool = torch.randint(0, 256, (num_pages, nkv, 2, 9 * d), dtype=torch.uint8, device=dev, generator=g)
+    pool[..., 8 * d:].view(torch.bfloat16).fill_(0.1)
+    assert pool[0].numel() == nf_kv4_page_bytes(nkv, d)
+    if args.op == "kv4_decode_attention":
+        size = nf_kv4_workspace_bytes(nq, nkv, d)
+        ws = torch.zeros(size, dtype=torch.uint8, device=dev)
+        q = randn(R, nq, d).to(torch.bfloat16)
+        o, lens, indptr, indices = torch.empty_like(q), i32(ctx + 1), i32(b.page_indptr[:R + 1]), i32(b.page_indices)
+        launch = lambda: check(nf_op_kv4_decode_attention(  # noqa: E731
+            q.data_ptr(), nq * d, o.data_ptr(), nq * d, pool.data_ptr(), num_pages, lens.data_ptr(), indptr.data_ptr(),
+            indices.data_ptr(), R, nq, nkv, d, 0.0, ws.data_ptr(), size, status.data_ptr(), args.sm, st), "kv4 attention")
+        return launch, {"requests": R}, int((ctx + 1).sum()) * nkv * d * 9 // 8 + 4 * R * nq * d, status
+    T = args.rows or R
+    slots = torch.randperm(num_pages * s.page_size, device=dev, generator=g)[:T].to(torch.int32)
+    T = slots.numel()
+    k, v = (randn(T, nkv, d).to(torch.bfloat16) for _ in range(2))
+    if args.op == "kv4_append":
+        launch = lambda: check(nf_op_kv4_append(  # noqa: E731
+            k.data_ptr(), nkv * d, NF_DTYPE_BF16, v.data_ptr(), nkv * d, NF_DTYPE_BF16, slots.data_ptr(), T,
+            pool.data_ptr(), num_pages, nkv, d, status.data_ptr(), st), "kv4 append")
+    else:
+        launch = lambda: check(nf_op_kv4_read(  # noqa: E731
+            pool.data_ptr(), num_pages, slots.data_ptr(), T, nkv, d, k.data_ptr(), nkv * d, v.data_ptr(), nkv * d,
+            NF_DTYPE_BF16, status.data_ptr(), st), "kv4 read")
+    return launch, {"rows": T}, T * nkv * d * (4 + 9 / 8), status
+
+
 def main(argv=None) -> dict:
     ap = argparse.ArgumentParser()
-    ap.add_argument("--op", choices=["decode_attention", "prefill_attention", "gemm", "iteration"], required=True)
+    ap.add_argument("--op", choices=["decode_attention", "prefill_attention", "gemm", "iteration", *KV4_OPS],
+                    required=True)
     ap.add_argument("--nano", type=int, default=1)
     ap.add_argument("--template", type=int, default=0)
     ap.add_argument("--sm-attn", type=int, default=0)
@@ -89,6 +163,7 @@ def main(argv=None) -> dict:
     ap.add_argument("--workload", default="llama3_8b_layer")
     ap.add_argument("--layers", type=int, default=0, help="build only this many layers of the workload (0: all)")
     ap.add_argument("--requests", type=int, default=0, help="decode requests (0 = all)")
+    ap.add_argument("--rows", type=int, default=0, help="rope, kv4_append, kv4_read: this many rows (0 = --requests)")
     ap.add_argument("--sm", type=int, default=0)
     ap.add_argument("--reps", type=int, default=5)
     ap.add_argument("--warmup", type=int, default=2)
@@ -116,6 +191,15 @@ def main(argv=None) -> dict:
         out.update({"shape": [M, N, K], "us": round(us, 2), "tflops": round(2.0 * M * N * K / us / 1e6, 1)})
         if args.power_s > 0:
             out["power"] = _power(launch, args.power_s, stream)
+    elif args.op in KV4_OPS:
+        from synth.workloads import WORKLOADS
+        launch, figures, nbytes, status = _kv4(args, WORKLOADS[args.workload], dev, stream)
+        us = _time(launch, args.reps, args.warmup, stream)
+        out.update({"workload": args.workload, **figures, "bytes": int(nbytes), "us": round(us, 2),
+                    "gbs": round(nbytes / us / 1e3, 1)})
+        if args.power_s > 0:
+            out["power"] = _power(launch, args.power_s, stream)
+        check(int(status.item()), "status")
     else:
         from synth.workloads import WORKLOADS
         from .harness import DeviceWorkload
