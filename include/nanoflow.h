@@ -489,8 +489,8 @@ nf_status nf_decode_attention_noalloc(const void* q, void* out, const void* kv_p
  * (p in 0..3, h in 0..1, t in 0..3, g in 0..7). No two slots share a byte. A pool needs no initial value:
  * slots that were never written are never read by a request whose length does not cover them.
  *
- * Common to these calls: device pointers of the current device (or managed memory; anything else is
- * NF_ERR_INVALID_ARGUMENT), row strides in elements between consecutive tokens, head h of a row at column
+ * Common to these calls: device pointers of the current device (or managed memory; anything else, or a
+ * pointer that is not aligned to its elements, is NF_ERR_INVALID_ARGUMENT), row strides in elements between consecutive tokens, head h of a row at column
  * h * head_dim. `status_device` (required) is an int32 that the caller zeroes; it receives the first error
  * that the device finds. All are asynchronous on `stream`, allocate nothing and may be captured into CUDA
  * graphs. NF_ERR_UNSUPPORTED for head dims other than 64 and 128, more than 256 KV heads or more than 8
@@ -511,9 +511,10 @@ nf_status nf_decode_attention_noalloc(const void* q, void* out, const void* kv_p
  *   page_indptr   [num_requests + 1], page_indices: the CSR page table of the a pages of each request;
  *   slots, positions  one entry per new token, request after request: its slot id and its position
  *                 (ctx_len[r] + i); entries behind the last token stay as they are;
- *   free_left     free_count[0] less the pages taken (a word of its own, free_left == free_count is refused;
- *                 pass it as free_count of the next step).
- * free_pages holds free_cap entries, page_indices page_cap, slots and positions token_cap each.
+ *   free_left     free_count[0] less the pages taken (pass it as free_count of the next step, which needs
+ *                 another word for its own free_left).
+ * free_pages holds free_cap entries, page_indices page_cap, slots and positions token_cap each. An array that is
+ * written may overlap no other one of the call (NF_ERR_INVALID_ARGUMENT): kv_len is not ctx_len.
  * A request is refused when its new pages, with those of all requests before it, exceed free_count
  * (NF_ERR_OUT_OF_MEMORY latched), or when ceil((ctx_len + new_len) / 16) > table_stride
  * (NF_ERR_DEVICE_BOUNDS): it takes no page, keeps kv_len = ctx_len and its old pages, and its tokens get
@@ -600,7 +601,7 @@ int64_t nf_kv4_workspace_bytes(int32_t n_q_heads, int32_t n_kv_heads, int32_t he
  * kv_len[r] is 0.
  *   q, out         bf16 rows [n_q_heads x head_dim], 16-byte aligned, strides multiples of 8 elements
  *   kv_len         device int32 [num_requests]; page_indptr, page_indices: CSR page table
- *   softmax_scale  0: 1 / sqrt(head_dim)
+ *   softmax_scale  0: 1 / sqrt(head_dim); NF_ERR_INVALID_ARGUMENT when negative or, times log2(e), not finite
  *   workspace      nf_kv4_workspace_bytes bytes, 256-byte aligned, zeroed by the caller once before its first
  *                  use; a call leaves it ready for the next one. Calls that may overlap on the GPU (other
  *                  streams, two captured graphs) need workspaces of their own.
@@ -608,8 +609,8 @@ int64_t nf_kv4_workspace_bytes(int32_t n_q_heads, int32_t n_kv_heads, int32_t he
  * NF_ERR_DEVICE_BOUNDS is latched for a negative kv_len (read as 0), a kv_len that the request's pages do not
  * hold (cut to them) and a page id outside the pool (its keys are left out). Scores, softmax statistics and
  * sums in fp32; the weights that multiply V, scaled by V's scales, are rounded to fp16 (2^-11). The order of
- * the sums follows the batch's lengths and sm_count, not the run: equal calls give equal bits. After
- * NF_ERR_DEVICE_TIMEOUT (a pipeline wait that passed its limit) the workspace has to be zeroed again. */
+ * the sums follows the batch's lengths and sm_count, not the run: equal calls give equal bits.
+ * num_pages * n_kv_heads is at most 2^31 - 1, else NF_ERR_INVALID_ARGUMENT. */
 nf_status nf_op_kv4_decode_attention(const void* q, int64_t q_stride, void* out, int64_t out_stride, const void* pool,
                                      int32_t num_pages, const int32_t* kv_len, const int32_t* page_indptr,
                                      const int32_t* page_indices, int32_t num_requests, int32_t n_q_heads,

@@ -1,6 +1,5 @@
 // Rows of K and V written to and read from the 4-bit paged cache (format: nf_kv4.h).
 #include <cstdint>
-#include <new>
 
 #include <cuda_runtime.h>
 
@@ -242,7 +241,7 @@ nf_status check_rows(const Kv4RowArgs& a, const void* k, const void* v, int32_t 
     // (warps are counted in 32 bits)
     if ((int64_t)a.T * a.nkv > 0x40000000) return NF_ERR_INVALID_ARGUMENT;
     if (a.T == 0) return NF_OK;
-    return check_on_device(k, v, (const void*)a.slots, (const void*)a.pool, (const void*)a.status);
+    return check_on_device(k, v, a.slots, a.pool, a.status);
 }
 
 }  // namespace

@@ -12,6 +12,8 @@
 // slots share a byte and rows can be written in parallel without read-modify-write.
 #pragma once
 #include <cstdint>
+#include <type_traits>
+
 #include <cuda_runtime.h>
 
 #include "nanoflow.h"
@@ -34,11 +36,17 @@ inline nf_status kv4_check_heads(int32_t nkv, int32_t d) {
 
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// NF_OK when every (non-null) pointer is memory of the current device (or managed), else
-// NF_ERR_INVALID_ARGUMENT; NF_ERR_CUDA without a device. A host pointer or another device's
-// would fault in the kernel. No stream operation: allowed while a stream is being captured.
+template <typename T>
+constexpr uintptr_t align_of() {
+    if constexpr (std::is_void_v<T>) return 1; else return alignof(T);
+}
+
+// NF_OK when every (non-null) pointer is aligned to its type and memory of the current device (or managed),
+// else NF_ERR_INVALID_ARGUMENT; NF_ERR_CUDA without a device. A host pointer, another device's or a misaligned
+// one would fault in the kernel. No stream operation: allowed while a stream is being captured.
 template <typename... P>
 nf_status check_on_device(const P*... ptrs) {
+    if (!(aligned(ptrs, align_of<P>()) && ...)) return NF_ERR_INVALID_ARGUMENT;
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return NF_ERR_CUDA; }
     const void* list[] = {ptrs...};
@@ -92,28 +100,6 @@ __device__ __forceinline__ void store_row8(T* row, const float* x) {
     } else {
         __stcs(reinterpret_cast<uint4*>(row), make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
                                                     pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
-    }
-}
-
-// Four consecutive values of a bf16 or fp32 row as fp32.
-template <typename T>
-__device__ __forceinline__ float4 load_row4(const void* row, int64_t at) {
-    if constexpr (sizeof(T) == 4) {
-        return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(row) + at));
-    } else {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(row) + at));
-        return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                           __uint_as_float(w.y & 0xFFFF0000u));
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ void store_row4(void* row, int64_t at, float4 v) {
-    if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4*>(static_cast<float*>(row) + at) = v;
-    } else {
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(row) + at) =
-            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     }
 }
 

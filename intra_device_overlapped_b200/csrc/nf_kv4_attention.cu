@@ -2,7 +2,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <new>
 
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -32,7 +31,6 @@ struct Kv4AttnArgs {
     const int *kv_len, *indptr, *indices;
     int R, nkv, G;
     float scale_log2;
-    uint32_t one;        // 0x3C003C00 (unpack4)
     int* arrived;        // [kMaxParts] parts of a (request, head) written so far, at its first part. 0 between calls
     float2* part_ml;     // [kMaxParts][kMaxGroup] maximum and sum
     float* part_o;       // [kMaxParts][G][D]
@@ -135,23 +133,22 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Codes of four pairs as fp16: nibble p of both halves of w, put under the exponent of 1: 1 + code / 1024 for the
-// even nibbles, which spare a shift, 1 + code / 64 for the odd ones. kExact takes the bias off again: (code - 8) /
-// 1024 and (code - 8) / 64, exactly. `one`, 0x3C003C00, comes as a value that the compiler does not know: with two
-// constants it makes two logic operations of each (64 more instructions a tile).
+// Codes of four pairs as fp16, nibble p of both halves of w as the last bits of a subnormal number: 2^-24 code for the
+// even nibbles, which spare a shift, 2^-20 code for the odd ones. kExact takes the bias off: 2^-24 (code - 8) and
+// 2^-20 (code - 8), exactly. (Under the exponent of 1 the bias would be 1032 and 72 codes, not 8.)
 template <bool kExact>
-__device__ __forceinline__ void unpack4(uint32_t w, uint32_t one, uint32_t* e) {
+__device__ __forceinline__ void unpack4(uint32_t w, uint32_t* e) {
     constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
     const uint32_t t = w >> 8;
-    e[0] = (w & kLow) | one;
-    e[1] = (w & kHigh) | one;
-    e[2] = (t & kLow) | one;
-    e[3] = (t & kHigh) | one;
+    e[0] = w & kLow;
+    e[1] = w & kHigh;
+    e[2] = t & kLow;
+    e[3] = t & kHigh;
     if constexpr (kExact) {
-        e[0] = sub_f16x2(e[0], 0x3C083C08u);
-        e[1] = sub_f16x2(e[1], 0x3C803C80u);
-        e[2] = sub_f16x2(e[2], 0x3C083C08u);
-        e[3] = sub_f16x2(e[3], 0x3C803C80u);
+        e[0] = sub_f16x2(e[0], 0x00080008u);
+        e[1] = sub_f16x2(e[1], 0x00800080u);
+        e[2] = sub_f16x2(e[2], 0x00080008u);
+        e[3] = sub_f16x2(e[3], 0x00800080u);
     }
 }
 
@@ -349,10 +346,10 @@ __device__ __noinline__ void join_parts(const Kv4AttnArgs& a, const Item& it, in
 // are stored in): no shared-memory round trip, which tcgen05 operands would need.
 //   Scores. S[key, head] = sum over groups j of s_k[key, j] * (sum over d in j of t q - b_j), t the codes as unpack4
 //   leaves them, q in fp16 times a power of two per head (exact but below 2^-24 of the row's largest; columns of the
-//   even nibbles times 16 for their codes' 1 / 1024), b_j = sum of bias times q. The scale is applied to the 16 x 8
+//   even nibbles times 16 for their codes' 2^-24), b_j = sum of bias times q. The scale is applied to the 16 x 8
 //   accumulator of each group, 32 columns, in fp32; -sum s_k b_j for all keys and heads is one more tensor
-//   instruction, the scales as stored times b_j in three bf16 terms (24 bits), and starts the sum. (The biased sums
-//   are at most about 100 times the result: 2^-17 of a score's spread.)
+//   instruction, the scales as stored times b_j in three bf16 terms (24 bits), and starts the sum. (Codes with their
+//   bias are at most 15 where the values reach 7: the sums lose one bit to it.)
 //   Output. O^T[d, head] += V^T[d, key] P^T[key, head], P = 2^(x - M) s_v[key, j] f_j in fp16 (2^-11), V's
 //   codes exact (their bias would meet the sum of all weights, which grows with the length while the result does
 //   not). f_j, a power of two that follows the largest scale of the group so far, and M, the integral running
@@ -495,7 +492,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
     };
 
     const int gid = lane >> 2, tig = lane & 3;
-    const uint32_t one = a.one;
     int pending = 0;  // parts written, to be reported
     for (int k = 0;; ++k) {
         if (flying < kStages) fill(k);
@@ -540,9 +536,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                 // 2^(10 - (ex - 127)) in two steps, either a normal number
                 const int up = 10 + 127 - ex, up0 = up / 2, up1 = up - up0;
                 const float m0 = __int_as_float((127 + up0) << 23), m1 = __int_as_float((127 + up1) << 23);
-                // (not 0, so that minus infinity times it stays that)
-                const float hs = fmaxf(a.scale_log2 * 64.f * __int_as_float((127 - up0) << 23) *
-                                           __int_as_float((127 - up1) << 23), 0x1p-140f);
+                // Not 0, so that minus infinity times it stays that, and finite: where the upper limit is met (|q| scale of
+                // 2^107 and more) scores that differ do so by 2^20 and more, with the limit as without.
+                const float hs = fminf(fmaxf(a.scale_log2 * __int_as_float((127 - up0) << 23) *
+                                                 __int_as_float((127 - up1) << 23) * 0x1p20f, 0x1p-140f), 0x1p127f);
                 hs0 = __shfl_sync(0xffffffffu, hs, 8 * tig);
                 hs1 = __shfl_sync(0xffffffffu, hs, 8 * tig + 4);
 #pragma unroll
@@ -553,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                         const float m = i % 2 ? m1 : m1 * 16.f;
                         qf[j][i] = pack_f16x2(lo_bf16(w[i]) * m0 * m, hi_bf16(w[i]) * m0 * m);
                         const __half2 back = *reinterpret_cast<__half2*>(&qf[j][i]);
-                        sum[j] -= (__low2float(back) + __high2float(back)) * (i % 2 ? 1.125f : 1.0078125f);
+                        sum[j] -= (__low2float(back) + __high2float(back)) * (i % 2 ? 0x1p-17f : 0x1p-21f);
                     }
                     sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
                     sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
@@ -610,8 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                             const uint32_t b0 = transpose8(pack_f16x2(yy[0] * ga, yy[1] * ga));
                             const uint32_t b1 = transpose8(pack_f16x2(yy[2] * gb, yy[3] * gb));
                             uint32_t ea[4], eb[4];
-                            unpack4<true>(va[2 * u + e], one, ea);
-                            unpack4<true>(vb[2 * u + e], one, eb);
+                            unpack4<true>(va[2 * u + e], ea);
+                            unpack4<true>(vb[2 * u + e], eb);
                             const uint32_t a0[4] = {ea[0], ea[1], eb[0], eb[1]}, a1[4] = {ea[2], ea[3], eb[2], eb[3]};
                             mma_f16(O[2 * u + e][0], a0, b0, b1, O[2 * u + e][0]);
                             mma_f16(O[2 * u + e][1], a1, b0, b1, O[2 * u + e][1]);
@@ -636,8 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
 #pragma unroll
                         for (int j = 0; j < NG; ++j) {
                             uint32_t ea[4], eb[4];
-                            unpack4<false>(ka[j], one, ea);
-                            unpack4<false>(kb[j], one, eb);
+                            unpack4<false>(ka[j], ea);
+                            unpack4<false>(kb[j], eb);
                             const uint32_t a0[4] = {ea[0], eb[0], ea[1], eb[1]}, a1[4] = {ea[2], eb[2], ea[3], eb[3]};
                             const float zero[4] = {0.f, 0.f, 0.f, 0.f};
                             float acc[4];
@@ -692,8 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                     const bool over = most > 5.f || lo_bf16(grown) >= 1024.f || hi_bf16(grown) >= 1024.f;
                     if (__any_sync(0xffffffffu, over)) {
                         // columns of heads beyond G are zeros throughout
-                        float n0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2])) * hs0;
-                        float n1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3])) * hs1;
+                        float n0 = __fmul_rn(fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2])), hs0);
+                        float n1 = __fmul_rn(fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3])), hs1);
                         uint32_t top[NW];
 #pragma unroll
                         for (int u = 0; u < NW; ++u)
@@ -732,12 +729,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                                 O[u][i][3] *= c1 * g;
                             }
                         }
+                        // rounded like the maximum: of a score beyond 2^27 the exact product may lie far above it
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            y[i][0] = fmaf(x[i][0], hs0, -M0);
-                            y[i][1] = fmaf(x[i][1], hs1, -M1);
-                            y[i][2] = fmaf(x[i][2], hs0, -M0);
-                            y[i][3] = fmaf(x[i][3], hs1, -M1);
+                            y[i][0] = __fmul_rn(x[i][0], hs0) - M0;
+                            y[i][1] = __fmul_rn(x[i][1], hs1) - M1;
+                            y[i][2] = __fmul_rn(x[i][2], hs0) - M0;
+                            y[i][3] = __fmul_rn(x[i][3], hs1) - M1;
                         }
                     }
                     load_v(0);
@@ -769,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
 #pragma unroll
         for (int u = 0; u < NG; ++u) {
             const uint32_t fu = u % 2 ? f[u / 2] >> 16 : f[u / 2] & 0xFFFFu;
-            const float g = over_pow2(6, fu), ge = over_pow2(10, fu);
+            const float g = over_pow2(20, fu), ge = over_pow2(24, fu);
             const float4 o0 = make_float4(O[u][0][0] * ge, O[u][0][2] * g, O[u][1][0] * ge, O[u][1][2] * g);
             const float4 o1 = make_float4(O[u][0][1] * ge, O[u][0][3] * g, O[u][1][1] * ge, O[u][1][3] * g);
             const int col = 32 * u + 4 * gid;
@@ -894,29 +892,29 @@ extern "C" nf_status nf_op_kv4_decode_attention(const void* q, int64_t q_stride,
     if (st != NF_OK) return st;
     const int64_t row = (int64_t)n_q_heads * head_dim;
     // (tiles are numbered page * n_kv_heads + head in 32 bits: a pool of 2^31 tiles would not fit any device)
-    if (num_pages < 1 || num_pages > NF_KV4_MAX_PAGES || (int64_t)num_pages * n_kv_heads > 0x7fffffff || num_requests < 0 || num_requests > NF_KV4_MAX_REQUESTS ||
-        sm_count < 0 || !(softmax_scale >= 0.f) || !std::isfinite(softmax_scale))
+    if (num_pages < 1 || num_pages > NF_KV4_MAX_PAGES || (int64_t)num_pages * n_kv_heads > 0x7fffffff ||
+        num_requests < 0 || num_requests > NF_KV4_MAX_REQUESTS || sm_count < 0)
         return NF_ERR_INVALID_ARGUMENT;
+    const double scale = softmax_scale != 0.f ? (double)softmax_scale : 1.0 / std::sqrt((double)head_dim);
+    const float scale_log2 = (float)(scale * 1.4426950408889634);
+    if (!(scale > 0.0) || !std::isfinite(scale_log2)) return NF_ERR_INVALID_ARGUMENT;
     if (q_stride < row || out_stride < row || q_stride % 8 || out_stride % 8 || !nf::aligned(q, 16) ||
         !nf::aligned(out, 16) || !nf::aligned(pool, 16) || !nf::aligned(workspace, 256) ||
         workspace_bytes < nf_kv4_workspace_bytes(n_q_heads, n_kv_heads, head_dim))
         return NF_ERR_INVALID_ARGUMENT;
     if (num_requests == 0) return NF_OK;
-    if ((st = nf::check_on_device(q, (const void*)out, pool, (const void*)kv_len, (const void*)page_indptr,
-                                  (const void*)page_indices, (const void*)workspace, (const void*)status_device)) !=
-        NF_OK)
+    if ((st = nf::check_on_device(q, out, pool, kv_len, page_indptr, page_indices, workspace, status_device)) != NF_OK)
         return st;
     int sms = nf::device_sm_count();
     if (sms <= 0) return NF_ERR_CUDA;
     if (sm_count > 0 && sm_count < sms) sms = sm_count;
     const int grid = std::min(sms, nf::kMaxCtas);
-    const double scale = softmax_scale > 0.f ? (double)softmax_scale : 1.0 / std::sqrt((double)head_dim);
     const int G = n_q_heads / n_kv_heads;
     const nf::Workspace at(G, head_dim);
     uint8_t* w = static_cast<uint8_t*>(workspace);
     const nf::Kv4AttnArgs a{static_cast<const uint16_t*>(q), static_cast<uint16_t*>(out), q_stride, out_stride,
                             static_cast<const uint8_t*>(pool), num_pages, kv_len, page_indptr, page_indices,
-                            num_requests, n_kv_heads, G, (float)(scale * 1.4426950408889634), 0x3C003C00u,
+                            num_requests, n_kv_heads, G, scale_log2,
                             reinterpret_cast<int*>(w + at.arrived), reinterpret_cast<float2*>(w + at.ml),
                             reinterpret_cast<float*>(w + at.o), status_device};
     cudaStream_t s = static_cast<cudaStream_t>(stream);

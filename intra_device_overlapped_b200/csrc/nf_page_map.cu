@@ -30,6 +30,15 @@ struct PageMapArgs {
     int* status;
 };
 
+struct Span {  // n words from p
+    const int* p;
+    int64_t n;
+    bool meets(const Span& b) const {
+        return n > 0 && b.n > 0 && reinterpret_cast<uintptr_t>(p) < reinterpret_cast<uintptr_t>(b.p) + 4 * b.n &&
+               reinterpret_cast<uintptr_t>(b.p) < reinterpret_cast<uintptr_t>(p) + 4 * n;
+    }
+};
+
 struct Need {
     int ctx, fresh;  // cached tokens, new tokens
     int before;      // pages of the cached tokens
@@ -210,7 +219,18 @@ extern "C" nf_status nf_op_page_map(const int32_t* ctx_len, const int32_t* new_l
     if (num_requests < 0 || num_requests > NF_KV4_MAX_REQUESTS || table_stride < 1 || free_cap < 0 || page_cap < 0 ||
         token_cap < 0 || num_pages < 1 || num_pages > NF_KV4_MAX_PAGES)
         return NF_ERR_INVALID_ARGUMENT;
-    if (free_left == free_count) return NF_ERR_INVALID_ARGUMENT;  // every CTA reads the count; one writes what is left
+    // every CTA reads all of the inputs while others write: an array that is written is a memory of its own
+    const nf::Span read[] = {{ctx_len, num_requests}, {new_len, new_len ? num_requests : 0}, {free_pages, free_cap},
+                             {free_count, 1}};
+    const nf::Span written[] = {{block_table, (int64_t)num_requests * table_stride}, {kv_len, num_requests},
+                                {page_indptr, (int64_t)num_requests + 1}, {page_indices, page_cap}, {slots, token_cap},
+                                {positions, token_cap}, {free_left, 1}};
+    for (const nf::Span& w : written) {
+        for (const nf::Span& r : read)
+            if (w.meets(r)) return NF_ERR_INVALID_ARGUMENT;
+        for (const nf::Span& other : written)
+            if (&other != &w && w.meets(other)) return NF_ERR_INVALID_ARGUMENT;
+    }
     const nf_status st = nf::check_on_device(ctx_len, new_len, block_table, free_pages, free_count, kv_len, page_indptr,
                                              page_indices, slots, positions, free_left, status_device);
     if (st != NF_OK) return st;

@@ -1,7 +1,6 @@
 // Rotary positions: frequencies (host) and the rotation of rows of q and k heads.
 #include <cmath>
 #include <cstdint>
-#include <new>
 
 #include <cuda_runtime.h>
 
@@ -107,8 +106,8 @@ template <typename TI, typename TO>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     __shared__ float2 cs[kRopeMaxDim / 2];
     const int half = a.rot / 2;
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-        form_turns(a, t, cs, threadIdx.x, kRopeThreads);
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        form_turns(a, (int)t, cs, threadIdx.x, kRopeThreads);
         __syncthreads();
         const int units = a.d / 2, heads = a.q.heads + a.k.heads;
         for (int e = threadIdx.x; e < heads * units; e += kRopeThreads) {
@@ -116,8 +115,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
             const bool isq = h < a.q.heads;
             const RopeSide& side = isq ? a.q : a.k;
             const int hh = isq ? h : h - a.q.heads;
-            const TI* x = static_cast<const TI*>(side.in) + (int64_t)t * side.in_stride + (int64_t)hh * a.d;
-            TO* y = static_cast<TO*>(side.out) + (int64_t)t * side.out_stride + (int64_t)hh * a.d;
+            const TI* x = static_cast<const TI*>(side.in) + t * side.in_stride + (int64_t)hh * a.d;
+            TO* y = static_cast<TO*>(side.out) + t * side.out_stride + (int64_t)hh * a.d;
             int i, j;
             if (u >= half) { i = 2 * u; j = i + 1; }
             else if (a.interleaved) { i = 2 * u; j = i + 1; }
@@ -154,7 +153,7 @@ cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
         if (a.T < 4096)
             rope_vec_kernel<TI, TO, 1><<<a.T, kRopeThreads, 0, s>>>(a, per_token, per_head);
         else
-            rope_vec_kernel<TI, TO, 4><<<(a.T + 3) / 4, kRopeThreads, 0, s>>>(a, per_token, per_head);
+            rope_vec_kernel<TI, TO, 4><<<(a.T - 1) / 4 + 1, kRopeThreads, 0, s>>>(a, per_token, per_head);
     } else {
         const int grid = a.T < 148 * 8 ? a.T : 148 * 8;
         rope_kernel<TI, TO><<<grid, kRopeThreads, 0, s>>>(a);
@@ -260,7 +259,7 @@ extern "C" nf_status nf_op_rope(const void* q, int64_t q_stride, void* q_out, in
         return NF_ERR_INVALID_ARGUMENT;
     if (num_tokens == 0 || n_q_heads + n_kv_heads == 0) return NF_OK;
     if ((st = nf::check_on_device(n_q_heads ? q : nullptr, n_q_heads ? q_out : nullptr, n_kv_heads ? k : nullptr,
-                                  n_kv_heads ? k_out : nullptr, (const void*)positions, (const void*)inv_freq)) != NF_OK)
+                                  n_kv_heads ? k_out : nullptr, positions, inv_freq)) != NF_OK)
         return st;
     a.positions = positions;
     a.freq = inv_freq;

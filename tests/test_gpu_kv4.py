@@ -398,13 +398,15 @@ def _attend(nf, c, q, out, ws, status, scale=0.0, sm=0, stream=0, R=None):
 
 def _check_attention(c, q, got, scale=None, rows=None):
     """Against 64 bits, element by element. The output rounds once to bf16 (2^-8 of it); each weight, scaled by V's
-    scale, rounds to fp16 (2^-11); scores are fp32 sums of q times (code + bias) / 64 in units of 64 scales, 40
-    roundings of at most 2^-23 (16-term tensor-core steps cut off) of sums that are at most |q| (|k| + 80 scale) per
-    column, and a weight's relative error is twice (numerator, sum) that of its exponent; ex2 adds 2^-22 and the sums
-    2^-22 more. A scaled weight w s f, f in [2^8, 2^10) / (the group's largest scale), cannot be nearer than fp16's
-    least step allows, 2^-25: times |code| <= 8, over f and the sum of the weights (at least 1/2: the maximum is the
-    ceiling of a score at most) that is 2^-29 of the group's largest scale for each key, where the keys that weigh most
-    have codes of 0."""
+    scale, rounds to fp16 (2^-11). A score is an fp32 sum of q (code + 8) less one of 8 q: at most |q| times 15 + 8
+    scales a column. Its roundings, in units of 2^-23 of that: 2 for the tensor-core steps of a group and 1 for that of
+    the biases, 5 for the 10 additions of a group's bias, 1/2 for its split in three terms, 2 for 4 joins of groups:
+    less than 11. (A scale is a seventh of its group's largest value or less; the bound takes the value itself for it,
+    for steps of the tensor core that lose more.) A weight's relative error is twice (numerator, sum) that of its
+    exponent; ex2 adds 2^-22 and the sums 2^-22 more. A scaled weight w s f, f in [2^8, 2^10) / (the group's largest
+    scale), cannot be nearer than fp16's least step allows, 2^-25: times |code| <= 8, over f and the sum of the weights
+    (at least 1/2: the maximum is the ceiling of a score at most) that is 2^-29 of the group's largest scale for each
+    key, where the keys that weigh most have codes of 0."""
     d, nkv = c.d, c.nkv
     G = q.shape[1] // nkv
     sc = 1.0 / math.sqrt(d) if scale is None else scale
@@ -419,7 +421,7 @@ def _check_attention(c, q, got, scale=None, rows=None):
             qq = qh[r, h * G:(h + 1) * G]
             want, mass = ref.attention(qq, K[h], V[h], sc)
             unit = np.abs(K[h]).reshape(len(K[h]), -1, 32).max(-1).repeat(32, -1)    # at least a scale, or a zero group
-            x_err = 40 * 2.0 ** -23 * sc * (np.abs(qq) @ (np.abs(K[h]) + 80 * unit).T).max(-1)
+            x_err = 11 * 2.0 ** -23 * sc * (np.abs(qq) @ (23 * unit).T).max(-1)
             bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * x_err[:, None] + 2.0 ** -21) * mass
             # (some code of a group of 32 is not 0: its largest value is at least its scale)
             bound += 2.0 ** -29 * len(V[h]) * np.abs(V[h]).max(0).reshape(-1, 32).max(-1).repeat(32)
@@ -487,6 +489,30 @@ def test_attention_at_far_magnitudes(nf, qs, vs):
     _attend(nf, c, q, out, ws, status)
     torch.cuda.synchronize()
     _check_attention(c, q, out)
+
+
+@pytest.mark.parametrize("qs", [2.0 ** 60, 2.0 ** 100, 2.0 ** 112, 2.0 ** 118, 2.0 ** 122])
+def test_attention_of_huge_scores_takes_the_largest(nf, qs):
+    """Scores up to 2^80, far apart: one key has all the weight, the others' underflow."""
+    c = Cache([200, 17, 33], 2, 128, seed=16, spread=2.0 ** -45)
+    x = np.random.default_rng(3).standard_normal((3, 8, 128)) * qs
+    q = _dev(x.astype(np.float32), torch.bfloat16)
+    out, ws, status = torch.empty_like(q), _workspace(nf, 8, 2, 128), _status()
+    _attend(nf, c, q, out, ws, status)
+    torch.cuda.synchronize()
+    qh, gh = _host(q), _host(out)
+    for r in range(3):
+        K, V = c.keys(r)
+        for h in range(8):
+            s = K[h // 4] @ qh[r, h] / math.sqrt(128)
+            order = np.argsort(s)
+            # the rounding of a score (_check_attention) cannot change the order, and the next weight is below 2^-100
+            err = 11 * 2.0 ** -23 * 23 * (np.abs(K[h // 4]).max() * np.abs(qh[r, h]).sum()) / math.sqrt(128)
+            if s[order[-1]] - s[order[-2]] <= 2 * err + 100:
+                continue
+            want = V[h // 4][order[-1]]
+            # one weight, 1 of 1 but for its rounding to fp16 and that of the output
+            assert (np.abs(gh[r, h] - want) <= (2.0 ** -8 + 2.0 ** -11) * np.abs(want) + 2.0 ** -29 * np.abs(V[h // 4]).max()).all(), (r, h)
 
 
 def test_attention_mixed_v_scales_in_one_row(nf):

@@ -65,7 +65,7 @@ def test_memory_of_no_device_is_refused(call):
     (dict(T=-1), BAD), (dict(nq=-1), BAD), (dict(nkv=-1), BAD), (dict(d=127), BAD), (dict(rot=63), BAD),
     (dict(rot=0), BAD), (dict(rot=130), BAD), (dict(inter=2), BAD), (dict(idt=2), BAD), (dict(odt=-1), BAD),
     (dict(qs=511), BAD), (dict(kos=255), BAD), (dict(q=P + 1), BAD), (dict(ko=P * 4 + 2, odt=1), BAD),
-    (dict(scale=math.nan), BAD), (dict(qo=P, qos=520), BAD), (dict(ko=P * 3, odt=1), BAD),
+    (dict(pos=P * 5 + 2), BAD), (dict(freq=P * 6 + 4), BAD), (dict(scale=math.nan), BAD), (dict(qo=P, qos=520), BAD), (dict(ko=P * 3, odt=1), BAD),
     (dict(d=514, rot=2, qs=4096, qos=4096, ks=4096, kos=4096), UNSUP), (dict(T=0), 0),
     (dict(nq=0, nkv=0, q=0, k=0, qo=0, ko=0), 0)])
 def test_rope_refusals(kw, want):
@@ -78,7 +78,8 @@ def test_rope_refusals(kw, want):
     (dict(T=-1), BAD), (dict(pages=0), BAD), (dict(pages=nf.NF_KV4_MAX_PAGES + 1), BAD), (dict(dt=2, vdt=2), BAD),
     (dict(nkv=0), BAD), (dict(d=0), BAD), (dict(d=96), UNSUP), (dict(nkv=257, ks=1 << 20, vs=1 << 20), UNSUP),
     (dict(ks=252), BAD), (dict(vs=258), BAD), (dict(k=P + 4), BAD), (dict(v=P + 8, dt=1, vdt=1), BAD), (dict(pool=P + 8), BAD),
-    (dict(ks=260), BAD), (dict(T=1 << 30), BAD), (dict(T=0), 0)])
+    (dict(ks=260), BAD), (dict(slots=P * 3 + 2), BAD), (dict(status=P * 5 + 1), BAD), (dict(T=1 << 30), BAD),
+    (dict(T=0), 0)])
 def test_row_refusals(read, kw, want):
     assert _append(read, **kw) == want
 
@@ -88,7 +89,9 @@ def test_row_refusals(read, kw, want):
     (dict(ws=0), BAD), (dict(status=0), BAD), (dict(pages=0), BAD), (dict(R=-1), BAD),
     (dict(R=nf.NF_KV4_MAX_REQUESTS + 1), BAD), (dict(nq=0), BAD), (dict(nq=9), BAD), (dict(nkv=0), BAD),
     (dict(d=96), UNSUP), (dict(nq=18, qs=4096, os=4096), UNSUP), (dict(scale=-1.0), BAD), (dict(scale=math.nan), BAD),
-    (dict(scale=math.inf), BAD), (dict(qs=1016), BAD), (dict(os=1028), BAD), (dict(q=P + 8), BAD),
+    (dict(scale=math.inf), BAD), (dict(scale=3e38), BAD), (dict(pages=(1 << 30) + 1, nkv=2), BAD),
+    (dict(pages=1 << 26, nkv=32, nq=32, qs=4096, os=4096, size=1 << 30), BAD), (dict(kv=P * 4 + 1), BAD),
+    (dict(ip=P * 5 + 2), BAD), (dict(ix=P * 6 + 2), BAD), (dict(status=P * 8 + 2), BAD), (dict(qs=1016), BAD), (dict(os=1028), BAD), (dict(q=P + 8), BAD),
     (dict(out=P * 2 + 8), BAD), (dict(pool=P * 3 + 8), BAD), (dict(ws=P * 7 + 128), BAD), (dict(size=16), BAD),
     (dict(sm=-1), BAD), (dict(R=0), 0)])
 def test_attention_refusals(kw, want):
@@ -99,9 +102,18 @@ def test_attention_refusals(kw, want):
     dict(ctx=0), dict(table=0), dict(free=0), dict(count=0), dict(kv=0), dict(ip=0), dict(ix=0), dict(slots=0),
     dict(pos=0), dict(left=0), dict(status=0), dict(R=-1), dict(R=nf.NF_KV4_MAX_REQUESTS + 1), dict(stride=0),
     dict(cap=-1), dict(pcap=-1), dict(tcap=-1), dict(pages=0), dict(pages=nf.NF_KV4_MAX_PAGES + 1),
-    dict(left=P * 4)])
+    dict(left=P * 4),
+    # arrays that are written and overlap others
+    dict(kv=P), dict(kv=P + 8), dict(new=P * 5), dict(ip=P * 3 + 32), dict(slots=P * 9 - 4), dict(pos=P * 8 + 116),
+    dict(table=P * 3 - 92), dict(left=P * 5 + 8), dict(left=P * 7 + 116), dict(kv=P * 6 + 12), dict(ix=P * 8 - 116),
+    # not aligned to their elements
+    dict(ctx=P + 1), dict(new=P * 12 + 2), dict(table=P * 2 + 2), dict(count=P * 4 + 3), dict(slots=P * 8 + 2)])
 def test_page_map_refusals(kw):
     assert _map(**kw) == BAD
+
+
+def test_page_map_arrays_next_to_one_another_are_taken():
+    assert _map(kv=P + 12, left=P * 9 - 4, table=P * 3 - 96) == (BAD if torch.cuda.is_available() else nf.NF_ERR_CUDA)
 
 
 def test_sizes():
