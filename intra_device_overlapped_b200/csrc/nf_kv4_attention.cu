@@ -20,6 +20,7 @@ constexpr int kStages = 2;                 // pairs of tiles in flight per warp
 constexpr int kMaxCtas = 160;              // sizes the workspace (a B200 has 148 SMs)
 constexpr int kMinShare = 4;               // places of a worker at least (Deal)
 constexpr int kOverhead = 10;              // what beginning and ending a (request, head) costs, in pages
+constexpr int kWeightBits = 5, kScaleBits = 5;  // (Output, below) their sum and the slack of 5 make P < 2^15
 constexpr int kMaxParts = 2 * kWarps * kMaxCtas;
 
 struct Kv4AttnArgs {
@@ -152,16 +153,18 @@ __device__ __forceinline__ void unpack4(uint32_t w, uint32_t* e) {
     }
 }
 
+// both halves of a times half `h` of b
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b, int h) {
+    const __half2 s = *reinterpret_cast<__half2*>(&b);
+    const __half2 r = __hmul2_rn(*reinterpret_cast<__half2*>(&a), h ? __high2half2(s) : __low2half2(s));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // Transpose of an 8 x 8 matrix of 16-bit values (two of a row to a lane)
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
     uint32_t d;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
-}
-
-// 2^n / f for a power of two f that a bf16 holds
-__device__ __forceinline__ float over_pow2(int n, uint32_t f_bits) {
-    return __int_as_float((n + 254 - (int)(f_bits >> 7)) << 23);
 }
 
 template <int N>
@@ -173,10 +176,10 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
+// Two bf16 scales as fp16, times 2^(112 - o) with off = o << 7 of each: the exponent moved, both fields shifted into
+// place. Below the normal numbers of fp16 it is 0 (or, in the last step above, less than it should be), NaN stays NaN.
+__device__ __forceinline__ uint32_t scales_f16(uint32_t w, uint32_t off) {
+    return __viaddmin_s16x2_relu(w, off, 0x0FC00FC0u) << 3;
 }
 
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
@@ -350,11 +353,16 @@ __device__ __noinline__ void join_parts(const Kv4AttnArgs& a, const Item& it, in
 //   accumulator of each group, 32 columns, in fp32; -sum s_k b_j for all keys and heads is one more tensor
 //   instruction, the scales as stored times b_j in three bf16 terms (24 bits), and starts the sum. (Codes with their
 //   bias are at most 15 where the values reach 7: the sums lose one bit to it.)
-//   Output. O^T[d, head] += V^T[d, key] P^T[key, head], P = 2^(x - M) s_v[key, j] f_j in fp16 (2^-11), V's
-//   codes exact (their bias would meet the sum of all weights, which grows with the length while the result does
-//   not). f_j, a power of two that follows the largest scale of the group so far, and M, the integral running
-//   maximum of the head, keep P within 2^15; both move only when a value has outgrown them (2^5 and 2^2 of slack),
-//   which one vote per two tiles detects. P goes from accumulator to operand layout by movmatrix.
+//   Output. O^T[d, head] += V^T[d, key] P^T[key, head], P = rn(2^(x - M)) s_v[key, j] f_j, both factors and their product
+//   in fp16 (2^-11 for the first, 2^-11 for the product; s_v f_j is exact), V's codes exact (their bias would meet the sum
+//   of all weights, which grows with the length while the result does not). Products in packed halves take 18
+//   instructions a tile fewer than in fp32: 161 us for 512 requests of 1280 keys, else 167. f_j, a power of two that
+//   follows the largest scale of the group so far, is taken into a scale's exponent by integer arithmetic; M is the
+//   integral running maximum of the head less 5. They keep scales below 2^5 (the largest at 2^3 or more), weights below
+//   2^10 (the largest at 2^4 or more) and P below 2^15, and move only when a value has outgrown its limit, which one vote
+//   per two tiles detects. Below: weights cannot be nearer than 2^-25, P neither, scales under 2^-14 count as 0: 2^-26
+//   and 2^-29 of the group's largest scale a key, and 2^-14 of it in all. P goes from accumulator to operand layout by
+//   movmatrix.
 // Sums and statistics are fp32. M0, M1 etc. belong to the two head columns 2 t, 2 t + 1 of a lane.
 //
 // Work. Each CTA scans the lengths itself (no second launch, nothing on the host depends on them). With many (request,
@@ -425,49 +433,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
 
     // --- this warp's stretches and its ring of tile pairs. Pair i is pages step i + offset and the next one.
     const int step = team ? 2 * kWarps : 2, offset = team ? 2 * warp : 0;
+    static_assert(kStages == 2, "stages are told apart by one bit");
+    constexpr int kStage = 2 * S::kHead;
     int flying = 0;                // pairs on their way or waiting: cp.async groups in flight at most
-    uint32_t absent = 0;           // two bits per stage: no such page, or one outside the pool
-    int in_st = 0, out_st = 0;     // stages of the next pair issued, used
+    uint32_t absent = 0;           // two bits per pair on its way, the next one lowest: no such page, or one outside the pool
+    int out_st = 0;                // offset of the stage of the next pair used
     int ahead = 0;                 // stretches begun to load; of the last of them:
-    int rem = 0, head = 0;         // pages from the next pair on, its head
+    int rem = 0;                   // pages from the next pair on
     const int* idp = a.indices;    // their places in the page table
-    int id0 = -1, id1 = -1;        // the next pair's pages, fetched while the pair before is worked on
-    const uint32_t my_ring = smem_u32(s.ring[warp]) + lane * 16;
-    const uint8_t* const my_pool = a.pool + lane * 16;
-    auto fetch_ids = [&]() {
-        id0 = rem > 0 ? __ldg(idp) : -1;
-        id1 = rem > 1 ? __ldg(idp + 1) : -1;
-    };
+    int id = -1;                   // of its pages, the one that the lane copies, fetched while the pair before is worked on
+    // half a warp copies a tile: 16 bytes a lane at a time
+    const int half = lane >> 4;
+    const uint32_t my_ring = smem_u32(s.ring[warp]) + half * S::kHead + (lane & 15) * 16;
+    const uint8_t* from = a.pool;  // the lane's first 16 bytes of the head's tile of page 0
+    const int page = a.nkv * S::kHead;
+    auto fetch_id = [&]() { id = rem > half ? __ldg(idp) : -1; };
     auto issue = [&]() {  // the next pair's tiles (rem > 0)
-        const bool bad0 = (unsigned)id0 >= (unsigned)a.num_pages, bad1 = (unsigned)id1 >= (unsigned)a.num_pages;
-        const uint32_t dst = my_ring + in_st * 2 * S::kHead;
-        const uint8_t* src0 = my_pool + ((int64_t)id0 * a.nkv + head) * S::kHead;
-        const uint8_t* src1 = my_pool + ((int64_t)id1 * a.nkv + head) * S::kHead - S::kHead;
-        constexpr int kPieces = (2 * S::kHead + 511) / 512;  // piece lane + 32 i of the two tiles, 16 bytes
-        absent &= ~(3u << 2 * in_st);
-        if (!bad0 && !bad1) {
+        const bool bad = (unsigned)id >= (unsigned)a.num_pages;
+        const uint32_t dst = my_ring + (flying ? out_st ^ kStage : out_st);
+        const uint8_t* src = from + (int64_t)id * page;
+        if (!bad) {
+            constexpr int kPieces = (S::kHead + 255) / 256;
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const bool second = 512 * i >= S::kHead || (512 * i + 512 > S::kHead && 512 * i + lane * 16 >= S::kHead);
-                if (512 * i + 512 <= 2 * S::kHead || 512 * i + lane * 16 < 2 * S::kHead)
-                    cp_async(dst + 512 * i, (second ? src1 : src0) + 512 * i);
-            }
-        } else {
-            if (bad0 || (bad1 && rem > 1)) set_status(a.status, NF_ERR_DEVICE_BOUNDS);
-            absent |= ((uint32_t)bad0 | (uint32_t)bad1 << 1) << 2 * in_st;
-#pragma unroll 1
-            for (int i = 0; i < kPieces; ++i) {
-                const int at = 512 * i + lane * 16;
-                if (at < S::kHead ? !bad0 : at < 2 * S::kHead && !bad1)
-                    cp_async(dst + 512 * i, (at < S::kHead ? src0 : src1) + 512 * i);
-            }
+            for (int i = 0; i < kPieces; ++i)
+                if (256 * i + 256 <= S::kHead || 256 * i + (lane & 15) * 16 < S::kHead) cp_async(dst + 256 * i, src + 256 * i);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
+        const uint32_t lost = __ballot_sync(0xffffffffu, bad);
+        if (lost) {
+            absent |= ((lost & 1) | (lost >> 31) << 1) << 2 * flying;
+            if ((lost & 1) || rem > 1) set_status(a.status, NF_ERR_DEVICE_BOUNDS);
+        }
         ++flying;
-        if (++in_st == kStages) in_st = 0;
         rem -= step;
         idp += step;
-        fetch_ids();
+        fetch_id();
     };
     auto fill = [&](int working) {  // `working`: the stretch that the warp works on
         while (flying < kStages) {
@@ -479,9 +479,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                 ++ahead;
                 rem = it.pages - offset;
                 if (rem <= 0) continue;
-                head = it.h;
-                idp = a.indices + it.first + offset;
-                fetch_ids();
+                from = a.pool + (int64_t)it.h * S::kHead + (lane & 15) * 16;
+                idp = a.indices + it.first + offset + half;
+                fetch_id();
                 // q of the stretch, in one group with its first tiles
                 const uint8_t* q = reinterpret_cast<const uint8_t*>(a.q + it.r * a.q_stride + (int64_t)it.h * a.G * D);
                 const uint32_t dst = smem_u32(s.q[warp][(ahead - 1) & 1]);
@@ -496,16 +496,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
     for (int k = 0;; ++k) {
         if (flying < kStages) fill(k);
         if (k >= ahead) break;
-        const int pages = s.item[warp][k & 1].pages, keys = s.item[warp][k & 1].keys;
+        const int keys = s.item[warp][k & 1].keys;
         float O[NG][2][4], M0 = -INFINITY, M1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-        uint32_t f[NW];
+        uint32_t f[NW];  // minus o << 7 of the groups: their scales count times 2^(112 - o)
 #pragma unroll
         for (int u = 0; u < NG; ++u) {
-            f[u / 2] = 0x71807180u;  // 2^100: the first scale outgrows it
+            f[u / 2] = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) O[u][0][i] = O[u][1][i] = 0.f;
         }
-        if (pages > offset) {
+        if (keys > offset * kKv4Slots) {
             if (flying == kStages)  // the first pair, and q with it
                 cp_async_wait<kStages - 1>();
             else
@@ -555,37 +555,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                     sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
                     sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
                 }
-                // -b_j of head gid in bf16 terms: rows 2 t, 2 t + 1 of the operand are groups 0, 1 (t even) or 2, 3
-                // (odd), for t < 2 the first term, then the second; rows 8 + 2 t .. the third (t < 2), then nothing
-                float lo = sum[0], hi = sum[1];
-                if (NW == 2 && (tig & 1)) {
-                    lo = sum[NG - 2];
-                    hi = sum[NG - 1];
-                }
-                const uint32_t first = pack_bf16x2(lo, hi);
-                lo -= lo_bf16(first);
-                hi -= hi_bf16(first);
-                const uint32_t second = pack_bf16x2(lo, hi);
-                lo -= lo_bf16(second);
-                hi -= hi_bf16(second);
-                const uint32_t third = pack_bf16x2(lo, hi);
-                if constexpr (NW == 2) {
-                    bias0 = tig < 2 ? first : second;
-                    bias1 = tig < 2 ? third : 0;
-                } else {
-                    bias0 = tig == 0 ? first : tig == 1 ? second : tig == 2 ? third : 0;
-                    bias1 = 0;
-                }
+                // -b_j of head gid in three bf16 terms, term t in rows 2 t, 2 t + 1 of the operand (groups 0, 1) and
+                // 8 + 2 t, 9 + 2 t (groups 2, 3)
+                auto term = [&](float lo, float hi) {
+                    uint32_t w = 0;
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        const uint32_t v = pack_bf16x2(lo, hi);
+                        lo -= lo_bf16(v);
+                        hi -= hi_bf16(v);
+                        if (i == tig) w = v;
+                    }
+                    return w;
+                };
+                bias0 = term(sum[0], sum[1]);
+                bias1 = NW == 2 ? term(sum[NG - 2], sum[NG - 1]) : 0;
             }
-            for (int p = offset; p < pages; p += step) {
+            for (int left = keys - offset * kKv4Slots; left > 0; left -= step * kKv4Slots) {  // keys from the pair on
                 if (flying < kStages) fill(k);  // (a new stretch to begin)
                 if (flying == kStages)
                     cp_async_wait<kStages - 1>();
                 else
                     cp_async_wait<0>();
                 __syncwarp();
-                const uint8_t* tile = s.ring[warp][out_st];
-                const uint32_t none = absent >> 2 * out_st & 3u;
+                const uint8_t* tile = s.ring[warp][0] + out_st;
+                const uint32_t none = absent & 3u;
                 uint32_t ta[2][NW], tb[2][NW], va[NG], vb[NG];
                 float y[2][4];
                 auto load_v = [&](int i) {
@@ -598,14 +592,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                     for (int e = 0; e < 4; ++e) yy[e] = ex2_approx(yy[e]);
                     l0 += yy[0] + yy[2];
                     l1 += yy[1] + yy[3];
+const uint32_t w0 = pack_f16x2(yy[0], yy[1]), w1 = pack_f16x2(yy[2], yy[3]);
 #pragma unroll
                     for (int u = 0; u < NW; ++u) {
-                        const uint32_t pa = mul_bf16x2(tta[u], f[u]), pb = mul_bf16x2(ttb[u], f[u]);
+                        const uint32_t pa = scales_f16(tta[u], f[u]), pb = scales_f16(ttb[u], f[u]);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float ga = e ? hi_bf16(pa) : lo_bf16(pa), gb = e ? hi_bf16(pb) : lo_bf16(pb);
-                            const uint32_t b0 = transpose8(pack_f16x2(yy[0] * ga, yy[1] * ga));
-                            const uint32_t b1 = transpose8(pack_f16x2(yy[2] * gb, yy[3] * gb));
+                            const uint32_t b0 = transpose8(mul_f16x2(w0, pa, e)), b1 = transpose8(mul_f16x2(w1, pb, e));
                             uint32_t ea[4], eb[4];
                             unpack4<true>(va[2 * u + e], ea);
                             unpack4<true>(vb[2 * u + e], eb);
@@ -625,11 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                         load_words<NG>(kt + 4 * D + lane * (D / 8), kb);    // slot gid + 8
                         load_scales<NG>(kt + 8 * D + gid * (2 * NG), sa);
                         load_scales<NG>(kt + 8 * D + (gid + 8) * (2 * NG), sb);
-                        {
-                            const uint32_t wa = NW == 2 && (tig & 1) ? sa[NW - 1] : sa[0];
-                            const uint32_t wb = NW == 2 && (tig & 1) ? sb[NW - 1] : sb[0];
-                            mma_bf16(x[i], wa, wb, wa, wb, bias0, bias1);
-                        }
+                        mma_bf16(x[i], sa[0], sb[0], sa[NW - 1], sb[NW - 1], bias0, bias1);
 #pragma unroll
                         for (int j = 0; j < NG; ++j) {
                             uint32_t ea[4], eb[4];
@@ -654,12 +643,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                         load_scales<NG>(vt + gid * (2 * NG), ta[i]);
                         load_scales<NG>(vt + (gid + 8) * (2 * NG), tb[i]);
                     }
-                    const int valid = keys - p * kKv4Slots;
-                    if (none || valid < 2 * kKv4Slots) {
+                    if (none || left < 2 * kKv4Slots) {
                         // slots behind the request's length, and of pages that are not there, hold anything
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const int n = none >> i & 1u ? 0 : valid - i * kKv4Slots;
+                            const int n = none >> i & 1u ? 0 : left - i * kKv4Slots;
                             if (gid >= n) {
                                 x[i][0] = x[i][1] = -INFINITY;
 #pragma unroll
@@ -672,11 +660,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                             }
                         }
                     }
+                    constexpr uint32_t kFull = (15 + kScaleBits) << 7;  // of a scale's bits less o << 7
                     uint32_t grown = 0;
 #pragma unroll
                     for (int u = 0; u < NW; ++u)
-                        grown = max_bf16x2(grown, mul_bf16x2(max_bf16x2(max_bf16x2(ta[0][u], tb[0][u]),
-                                                                        max_bf16x2(ta[1][u], tb[1][u])), f[u]));
+                        grown |= __viaddmax_s16x2(max_bf16x2(max_bf16x2(ta[0][u], tb[0][u]), max_bf16x2(ta[1][u], tb[1][u])),
+                                                  f[u], (kFull - 1) * 0x10001u) ^ (kFull - 1) * 0x10001u;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         y[i][0] = fmaf(x[i][0], hs0, -M0);
@@ -686,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                     }
                     const float most = fmaxf(fmaxf(fmaxf(y[0][0], y[0][1]), fmaxf(y[0][2], y[0][3])),
                                              fmaxf(fmaxf(y[1][0], y[1][1]), fmaxf(y[1][2], y[1][3])));
-                    const bool over = most > 5.f || lo_bf16(grown) >= 1024.f || hi_bf16(grown) >= 1024.f;
+                    const bool over = most > 5.f + kWeightBits || grown;
                     if (__any_sync(0xffffffffu, over)) {
                         // columns of heads beyond G are zeros throughout
                         float n0 = __fmul_rn(fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2])), hs0);
@@ -703,8 +692,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                             for (int u = 0; u < NW; ++u)
                                 top[u] = max_bf16x2(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
                         }
-                        n0 = softmax_max_update(M0, n0);
-                        n1 = softmax_max_update(M1, n1);
+                        n0 = softmax_max_update(M0, n0 - kWeightBits);
+                        n1 = softmax_max_update(M1, n1 - kWeightBits);
                         const float c0 = M0 == n0 ? 1.f : ex2_approx(M0 - n0), c1 = M1 == n1 ? 1.f : ex2_approx(M1 - n1);
                         M0 = n0;
                         M1 = n1;
@@ -712,14 +701,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                         l1 *= c1;
 #pragma unroll
                         for (int u = 0; u < NG; ++u) {
-                            const uint32_t was = u % 2 ? f[u / 2] >> 16 : f[u / 2] & 0xFFFFu;
-                            const float t = u % 2 ? hi_bf16(top[u / 2]) : lo_bf16(top[u / 2]);
+                            const int was = u % 2 ? (int)f[u / 2] >> 16 : (int)(short)f[u / 2];
+                            const int t = u % 2 ? top[u / 2] >> 16 : top[u / 2] & 0xFFFFu;
                             float g = 1.f;
-                            if (t * __uint_as_float(was << 16) >= 1024.f) {  // the new largest scale comes to [2^8, 2^9)
-                                const int e = (int)(__float_as_uint(t) >> 23);
-                                const uint32_t now = (uint32_t)min(max(254 + 8 - e, 1), 254) << 7;
-                                f[u / 2] = u % 2 ? (f[u / 2] & 0xFFFFu) | now << 16 : (f[u / 2] & 0xFFFF0000u) | now;
-                                g = __int_as_float(max(0, 127 + (int)(now >> 7) - (int)(was >> 7)) << 23);
+                            if (t + was >= (int)kFull) {  // the new largest scale comes to [2^-2, 2^-1) of the most
+                                const int now = -(min((t >> 7) - 13 - kScaleBits, 215) << 7);
+                                f[u / 2] = u % 2 ? (f[u / 2] & 0xFFFFu) | (uint32_t)now << 16
+                                                 : (f[u / 2] & 0xFFFF0000u) | ((uint32_t)now & 0xFFFFu);
+                                g = __int_as_float(max(0, 127 + ((now - was) >> 7)) << 23);
                             }
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
@@ -744,7 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                 }
                 __syncwarp();  // all read: the stage may be filled again
                 --flying;
-                if (++out_st == kStages) out_st = 0;
+                out_st ^= kStage;
+                absent >>= 2;
                 if (rem > 0) issue();
                 if (none != 3u) add_tile(y[1], ta[1], tb[1]);
             }
@@ -766,8 +756,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
         // rows of heads 2 t, 2 t + 1: columns 32 u + 4 g .. + 3
 #pragma unroll
         for (int u = 0; u < NG; ++u) {
-            const uint32_t fu = u % 2 ? f[u / 2] >> 16 : f[u / 2] & 0xFFFFu;
-            const float g = over_pow2(20, fu), ge = over_pow2(24, fu);
+            const int o = -(u % 2 ? (int)f[u / 2] >> 16 : (int)(short)f[u / 2]);
+            const float g = __int_as_float((127 + 20 - 112 << 23) + (o << 16)), ge = g * 16.f;
             const float4 o0 = make_float4(O[u][0][0] * ge, O[u][0][2] * g, O[u][1][0] * ge, O[u][1][2] * g);
             const float4 o1 = make_float4(O[u][0][1] * ge, O[u][0][3] * g, O[u][1][1] * ge, O[u][1][3] * g);
             const int col = 32 * u + 4 * gid;

@@ -397,16 +397,16 @@ def _attend(nf, c, q, out, ws, status, scale=0.0, sm=0, stream=0, R=None):
 
 
 def _check_attention(c, q, got, scale=None, rows=None):
-    """Against 64 bits, element by element. The output rounds once to bf16 (2^-8 of it); each weight, scaled by V's
-    scale, rounds to fp16 (2^-11). A score is an fp32 sum of q (code + 8) less one of 8 q: at most |q| times 15 + 8
+    """Against 64 bits, element by element. The output rounds once to bf16 (2^-8 of it); each weight rounds to
+    fp16 (2^-11), and again when scaled by V's scale. A score is an fp32 sum of q (code + 8) less one of 8 q: at most |q| times 15 + 8
     scales a column. Its roundings, in units of 2^-23 of that: 2 for the tensor-core steps of a group and 1 for that of
     the biases, 5 for the 10 additions of a group's bias, 1/2 for its split in three terms, 2 for 4 joins of groups:
     less than 11. (A scale is a seventh of its group's largest value or less; the bound takes the value itself for it,
     for steps of the tensor core that lose more.) A weight's relative error is twice (numerator, sum) that of its
-    exponent; ex2 adds 2^-22 and the sums 2^-22 more. A scaled weight w s f, f in [2^8, 2^10) / (the group's largest
-    scale), cannot be nearer than fp16's least step allows, 2^-25: times |code| <= 8, over f and the sum of the weights
-    (at least 1/2: the maximum is the ceiling of a score at most) that is 2^-29 of the group's largest scale for each
-    key, where the keys that weigh most have codes of 0."""
+    exponent; ex2 adds 2^-22 and the sums 2^-22 more. With S the group's largest scale so far, f in [2^3, 2^5) / S and
+    the largest weight w at 2^4 or more, neither w nor w s f can be nearer than fp16's least step allows, 2^-25. Times
+    |code| <= 8, over f and the sum of the weights (at least 2^4), that is 2^-26 of S (s <= S) and 2^-29 of S for each
+    key; s f below 2^-14 may be off by as much, for all keys together 2^-14 8 / f <= 2^-14 S."""
     d, nkv = c.d, c.nkv
     G = q.shape[1] // nkv
     sc = 1.0 / math.sqrt(d) if scale is None else scale
@@ -422,9 +422,9 @@ def _check_attention(c, q, got, scale=None, rows=None):
             want, mass = ref.attention(qq, K[h], V[h], sc)
             unit = np.abs(K[h]).reshape(len(K[h]), -1, 32).max(-1).repeat(32, -1)    # at least a scale, or a zero group
             x_err = 11 * 2.0 ** -23 * sc * (np.abs(qq) @ (23 * unit).T).max(-1)
-            bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * x_err[:, None] + 2.0 ** -21) * mass
+            bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -10 + 2 * x_err[:, None] + 2.0 ** -21) * mass
             # (some code of a group of 32 is not 0: its largest value is at least its scale)
-            bound += 2.0 ** -29 * len(V[h]) * np.abs(V[h]).max(0).reshape(-1, 32).max(-1).repeat(32)
+            bound += (2.0 ** -14 + (2.0 ** -26 + 2.0 ** -29) * len(V[h])) * np.abs(V[h]).max(0).reshape(-1, 32).max(-1).repeat(32)
             err = np.abs(gh[r, h * G:(h + 1) * G] - want)
             assert (err <= bound * (1 + 2.0 ** -6)).all(), (r, h, float((err / bound).max()))
             num, den = num + (err ** 2).sum(), den + (want ** 2).sum()
@@ -511,8 +511,9 @@ def test_attention_of_huge_scores_takes_the_largest(nf, qs):
             if s[order[-1]] - s[order[-2]] <= 2 * err + 100:
                 continue
             want = V[h // 4][order[-1]]
-            # one weight, 1 of 1 but for its rounding to fp16 and that of the output
-            assert (np.abs(gh[r, h] - want) <= (2.0 ** -8 + 2.0 ** -11) * np.abs(want) + 2.0 ** -29 * np.abs(V[h // 4]).max()).all(), (r, h)
+            # one weight, 1 of 1 but for the roundings to fp16 and that of the output
+            bound = (2.0 ** -8 + 2.0 ** -10) * np.abs(want) + 2.0 ** -13 * np.abs(V[h // 4]).max()
+            assert (np.abs(gh[r, h] - want) <= bound).all(), (r, h)
 
 
 def test_attention_mixed_v_scales_in_one_row(nf):
