@@ -50,8 +50,8 @@ struct Task {
             return false;
         }
         const int slot = id & 15;
-        const int at = which ? (slot >> 3) * 4 * D + ((slot & 7) >> 1) * D + 2 * (m & 3) * (D / 8) + 4 * (m >> 2) + 2 * (slot & 1)
-                             : slot * (D / 2) + (m & 3) * (D / 8) + 4 * (m >> 2);
+        const int at = (m & 3) * (D / 8) * (which ? 2 : 1) + 4 * (m >> 2) +
+                       (which ? (slot >> 3) * 4 * D + ((slot & 7) >> 1) * D + 2 * (slot & 1) : slot * (D / 2));
         scale = 8 * D + (slot * (D / 32) + (m >> 2)) * 2 - at;
         codes = a.pool + ((int64_t)(id >> 4) * a.nkv + h) * (2 * kv4_tile_bytes(D)) + which * kv4_tile_bytes(D) + at;
         return true;
@@ -105,7 +105,9 @@ __device__ __forceinline__ uint32_t shuffle_nibbles(uint32_t x) {
 
 // Append. A group's largest magnitude is found by 4 lanes, its scale by each of them; a K row's codes are written as 4-byte
 // words of 64 (32) consecutive bytes, a V row's as 2-byte units of 4 (2) sectors that two neighbouring slots share and L2
-// joins. All of a lane's rows are loaded before the first is quantised, and before its token's slot is known.
+// joins. All of a lane's rows are loaded before the first is quantised, and before its token's slot is known. 8192
+// rows of 8 heads of 128 take 13.5 us in bf16 (42 MB read, 9.4 written: 6.6 at a copy's rate), 13.8 in fp32 (11.7): bound
+// by instruction issue, 73 % of the slots, of which the rounding takes a third.
 template <int D, typename TK, typename TV>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowArgs a) {
     using W = Task<D>;
@@ -166,7 +168,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowArg
     }
 }
 
-// Read: the reverse. Bound by the rows written.
+// Read: the reverse. Bound by the rows written: 8192 rows of 8 heads of 128 in bf16 take 8.8 us (0.75 of a copy), 32768
+// 33.4 (0.79).
 template <int D, typename T>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4RowArgs a) {
     using W = Task<D>;

@@ -20,6 +20,7 @@ constexpr int kStages = 2;                 // pairs of tiles in flight per warp
 constexpr int kMaxCtas = 160;              // sizes the workspace (a B200 has 148 SMs)
 constexpr int kMinShare = 4;               // places of a worker at least (Deal)
 constexpr int kOverhead = 10;              // what beginning and ending a (request, head) costs, in pages
+constexpr int kJoin = 64, kJoinPart = 6;   // what a join by a warp costs, and each of its parts, in pages of a CTA
 constexpr int kWeightBits = 5, kScaleBits = 5;  // (Output, below) their sum and the slack of 5 make P < 2^15
 constexpr int kMaxParts = 2 * kWarps * kMaxCtas;
 
@@ -49,6 +50,11 @@ struct Item {
 
 __device__ __forceinline__ int part_slot(const Item& it, int c) { return c ? it.slot + 2 * c - 1 : it.slot; }
 
+// a / b of numbers from 0 on (the division of 64 bits takes about as long as a load from L2)
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    return (a | b) >> 32 ? a / b : (uint32_t)a / (uint32_t)b;
+}
+
 // How the pages are dealt: every (request, KV head) takes a number of places in one long order, worker w places
 // [w share, (w + 1) share). Warps as workers: a pair takes kOverhead places and one a page. CTAs ("team"): one place for
 // each `chunk` pages or less, and a share is one place.
@@ -59,7 +65,7 @@ struct Deal {
         return pages == 0 ? 0 : chunk ? (pages + chunk - 1) / chunk : (int64_t)pages + kOverhead;
     }
     __device__ __forceinline__ int worker_of(int64_t pos) const {
-        return (int)((pos | share) >> 32 ? pos / share : (uint32_t)pos / (uint32_t)share);
+        return (int)divide(pos, share);
     }
 };
 
@@ -73,6 +79,7 @@ struct Smem {
     Item item[kWarps][2], pending[kWarps][2];
     float2 ml[kWarps][kMaxGroup];
     int64_t scan[kWarps], start[kThreads + 1];
+    int64_t pos[kWarps];  // the place where the warp's next stretch begins
     Deal deal;
     int last[2];
 };
@@ -217,12 +224,15 @@ __device__ __forceinline__ void load_words(const uint8_t* at, uint32_t* w) {
 // 2^(m - M) for partial sums: a part without keys (m = -inf) holds zeros, or the NaN of a NaN score
 __device__ __forceinline__ float part_factor(float m, float M) { return m == -INFINITY ? 1.f : ex2_approx(m - M); }
 
-// The whole warp: the stretch that begins at place `pos` and ends with its (request, head) or at `stop`, the end of the
-// worker's share. Returns the place behind it; a stretch without pages (pos in the overhead before `stop`) has r = -1.
-// Kept out of line: it runs once a stretch and would cost the tile loop registers.
+// The whole warp: its next stretch, from s.pos to the end of a (request, head) or of the worker's share. r = -1: without
+// pages (s.pos in the overhead before the end of the share). Returns whether the share goes on behind it. Kept out of line
+// and its state in shared memory: it runs once a stretch and would cost the tile loop registers.
 template <int D>
-__device__ __noinline__ int64_t find_item(const Kv4AttnArgs& a, const Smem<D>& s, const Deal& deal, int64_t pos,
-                                          int64_t stop, int worker, int per, Item* out) {
+__device__ __noinline__ bool find_item(const Kv4AttnArgs& a, Smem<D>& s, Item* out) {
+    const Deal& deal = s.deal;
+    const int warp = threadIdx.x >> 5, worker = deal.chunk ? blockIdx.x : blockIdx.x * kWarps + warp;
+    const int per = (a.R + kThreads - 1) / kThreads;
+    const int64_t pos = s.pos[warp], stop = min(deal.total, (worker + 1) * deal.share);
     const int lane = threadIdx.x & 31;
     Item it;
     it.r = -1;
@@ -277,9 +287,13 @@ __device__ __noinline__ int64_t find_item(const Kv4AttnArgs& a, const Smem<D>& s
         }
         at = __shfl_sync(0xffffffffu, upto, 31);
     }
-    if (lane == 0) *out = it;
+    __syncwarp();  // (all have read s.pos)
+    if (lane == 0) {
+        *out = it;
+        s.pos[warp] = next;
+    }
     __syncwarp();
-    return next;
+    return next < stop;
 }
 
 // 4 columns of a head's output row from its sums
@@ -367,12 +381,20 @@ __device__ __noinline__ void join_parts(const Kv4AttnArgs& a, const Item& it, in
 //
 // Work. Each CTA scans the lengths itself (no second launch, nothing on the host depends on them). With many (request,
 // KV head) pairs a worker is a warp: the pages of all pairs, in order, are dealt to the warps (Deal), so that a share
-// covers some pairs whole and one at either end in part; no barrier, nothing shared. With at most half as many pairs as
-// CTAs a worker is a CTA ("team"): a pair is cut into equal chunks of at most pages / (CTAs - pairs), no more than there
-// are CTAs, whose pages go round the warps by twos and whose sums meet in shared memory. Every warp keeps its own ring of
+// covers some pairs whole and one at either end in part; no barrier, nothing shared. With fewer pairs
+// than CTAs a worker may be a CTA ("team"): a pair is cut into equal chunks of at most pages / (CTAs - pairs), no more than
+// there are CTAs, whose pages go round the warps by twos and whose sums meet in shared memory. That costs balance and
+// saves joins of many parts by one warp: 64 query heads on 8 KV heads, 8193 keys each, 1 request 16 us (warps as workers:
+// 68), 4 19.5 (37), 9 27 (37), 18 39.6 (49.7). A team is taken where its largest chunk is less than an equal share and
+// what the joins cost. Every warp keeps its own ring of
 // tiles full with cp.async (waits are for its own copies only) and runs up to one stretch ahead of the one it works on.
 // Parts of one pair meet in the workspace; a worker reports its parts, two at most, when its share is done, and whoever
 // brings the last one joins them, in order.
+//
+// Measured, calls back to back: 512 requests of 1024 to 1536 keys, 32 query and 8 KV heads of 128: 152 us, 0.76 of a copy
+// of the 761 MB; of 1 to 2048 keys 101 us (0.67); 2 of 131072 keys with 64 query heads 68 us (0.66). What bounds it is
+// the turning of codes into operands: about 290 instructions a tile, 58 % of the issue slots and half of the logic pipe in
+// use, with the 3 warps a scheduler that 168 registers allow to cover latencies (16 warps of 128 registers spill).
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid_constant__ Kv4AttnArgs a) {
     constexpr int NG = D / 32, NW = NG / 2;
@@ -383,10 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
 
     // --- the batch: how its pages are dealt, and the places before each thread's requests
     const int per = (a.R + kThreads - 1) / kThreads;
-    const bool team = 2 * (int64_t)a.R * a.nkv <= gridDim.x;
-    const int workers = team ? gridDim.x : gridDim.x * kWarps;
-    const int worker = team ? blockIdx.x : blockIdx.x * kWarps + warp;
     {
+        int workers = gridDim.x * kWarps;
         const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
         Deal d;
         d.chunk = 0;
@@ -404,16 +424,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
             }
             __syncthreads();
         };
-        if (team) {
-            for (int r = r0; r < r1; ++r) sum += pages_of(a, r, &keys, false);
+        const int64_t pairs = (int64_t)a.R * a.nkv;
+        if (pairs < gridDim.x) {  // (one request to a thread at most)
+            const int pages = r0 < r1 ? pages_of(a, r0, &keys, blockIdx.x == 0) : 0;
+            sum = pages;
             scan();
-            const int64_t others = workers - a.R * a.nkv;
-            d.chunk = (int)min(max((d.total + others - 1) / others, (int64_t)(2 * kWarps)), (int64_t)0x7fffffff);
-            sum = 0;
+            const int n = (int)pairs, others = gridDim.x - n;
+            d.chunk = (int)min(max(divide(d.total + others - 1, others), (int64_t)(2 * kWarps)), (int64_t)0x7fffffff);
+            // a team as long as its largest share is no more work than an equal one with the warps' joins
+            const int64_t most = divide(d.total, gridDim.x) + kJoin + kJoinPart * (workers / n);
+            if (__syncthreads_and(pages <= most * d.places(pages)))
+                workers = gridDim.x;
+            else
+                d.chunk = 0;
+            sum = d.places(pages);
+        } else {
+            for (int r = r0; r < r1; ++r) sum += d.places(pages_of(a, r, &keys, blockIdx.x == 0));
         }
-        for (int r = r0; r < r1; ++r) sum += d.places(pages_of(a, r, &keys, blockIdx.x == 0));
         scan();
-        d.share = team ? 1 : max((d.total + workers - 1) / workers, (int64_t)kMinShare);
+        d.share = d.chunk ? 1 : max(divide(d.total + workers - 1, workers), (int64_t)kMinShare);
         s.start[tid + 1] = before + upto;
         if (tid == 0) {
             s.start[0] = 0;
@@ -428,20 +457,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
             for (int i = tid * 8; i < a.nkv * a.G * D; i += kThreads * 8)
                 *reinterpret_cast<uint4*>(a.out + r * a.out_stride + i) = make_uint4(0, 0, 0, 0);
     }
-    int64_t pos = worker * s.deal.share;
-    const int64_t stop = min(s.deal.total, pos + s.deal.share);
+    // (read again where it is used: the loop has no register for it)
+    auto team = [&]() { return s.deal.chunk != 0; };
+    bool more;  // of the worker's share
+    {
+        const int worker = team() ? blockIdx.x : blockIdx.x * kWarps + warp;
+        const int64_t pos = worker * s.deal.share;
+        more = pos < s.deal.total;
+        if (lane == 0) s.pos[warp] = pos;
+        __syncwarp();
+    }
 
     // --- this warp's stretches and its ring of tile pairs. Pair i is pages step i + offset and the next one.
-    const int step = team ? 2 * kWarps : 2, offset = team ? 2 * warp : 0;
+    const int step = team() ? 2 * kWarps : 2;
+    auto offset = [&]() { return team() ? 2 * warp : 0; };
     static_assert(kStages == 2, "stages are told apart by one bit");
     constexpr int kStage = 2 * S::kHead;
     int flying = 0;                // pairs on their way or waiting: cp.async groups in flight at most
-    uint32_t absent = 0;           // two bits per pair on its way, the next one lowest: no such page, or one outside the pool
+    uint32_t absent = 0;           // two bits a pair on its way, the next one lowest: no such page, or not of the pool
     int out_st = 0;                // offset of the stage of the next pair used
     int ahead = 0;                 // stretches begun to load; of the last of them:
     int rem = 0;                   // pages from the next pair on
     const int* idp = a.indices;    // their places in the page table
-    int id = -1;                   // of its pages, the one that the lane copies, fetched while the pair before is worked on
+    int id = -1;                   // the page that the lane copies, fetched while the pair before is worked on
     // half a warp copies a tile: 16 bytes a lane at a time
     const int half = lane >> 4;
     const uint32_t my_ring = smem_u32(s.ring[warp]) + half * S::kHead + (lane & 15) * 16;
@@ -456,7 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
             constexpr int kPieces = (S::kHead + 255) / 256;
 #pragma unroll
             for (int i = 0; i < kPieces; ++i)
-                if (256 * i + 256 <= S::kHead || 256 * i + (lane & 15) * 16 < S::kHead) cp_async(dst + 256 * i, src + 256 * i);
+                if (256 * i + 256 <= S::kHead || 256 * i + (lane & 15) * 16 < S::kHead)
+                    cp_async(dst + 256 * i, src + 256 * i);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         const uint32_t lost = __ballot_sync(0xffffffffu, bad);
@@ -472,15 +511,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
     auto fill = [&](int working) {  // `working`: the stretch that the warp works on
         while (flying < kStages) {
             if (rem <= 0) {
-                if (pos >= stop || ahead > working + 1) return;
+                if (!more || ahead > working + 1) return;
                 Item& it = s.item[warp][ahead & 1];
-                pos = find_item<D>(a, s, s.deal, pos, stop, worker, per, &it);
+                more = find_item<D>(a, s, &it);
                 if (it.r < 0) continue;
                 ++ahead;
-                rem = it.pages - offset;
+                rem = it.pages - offset();
                 if (rem <= 0) continue;
                 from = a.pool + (int64_t)it.h * S::kHead + (lane & 15) * 16;
-                idp = a.indices + it.first + offset + half;
+                idp = a.indices + it.first + offset() + half;
                 fetch_id();
                 // q of the stretch, in one group with its first tiles
                 const uint8_t* q = reinterpret_cast<const uint8_t*>(a.q + it.r * a.q_stride + (int64_t)it.h * a.G * D);
@@ -505,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
 #pragma unroll
             for (int i = 0; i < 4; ++i) O[u][0][i] = O[u][1][i] = 0.f;
         }
-        if (keys > offset * kKv4Slots) {
+        if (keys > offset() * kKv4Slots) {
             if (flying == kStages)  // the first pair, and q with it
                 cp_async_wait<kStages - 1>();
             else
@@ -571,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                 bias0 = term(sum[0], sum[1]);
                 bias1 = NW == 2 ? term(sum[NG - 2], sum[NG - 1]) : 0;
             }
-            for (int left = keys - offset * kKv4Slots; left > 0; left -= step * kKv4Slots) {  // keys from the pair on
+            for (int left = keys - offset() * kKv4Slots; left > 0; left -= step * kKv4Slots) {  // keys from the pair on
                 if (flying < kStages) fill(k);  // (a new stretch to begin)
                 if (flying == kStages)
                     cp_async_wait<kStages - 1>();
@@ -746,7 +785,7 @@ const uint32_t w0 = pack_f16x2(yy[0], yy[1]), w1 = pack_f16x2(yy[2], yy[3]);
             l1 += __shfl_xor_sync(0xffffffffu, l1, o);
         }
         const Item it = s.item[warp][k & 1];
-        if (team) {  // (one stretch: the sums have their memory for themselves)
+        if (team()) {  // (one stretch: the sums have their memory for themselves)
             if (gid == 0) {
                 s.ml[warp][2 * tig] = make_float2(M0, l0);
                 s.ml[warp][2 * tig + 1] = make_float2(M1, l1);
@@ -761,7 +800,7 @@ const uint32_t w0 = pack_f16x2(yy[0], yy[1]), w1 = pack_f16x2(yy[2], yy[3]);
             const float4 o0 = make_float4(O[u][0][0] * ge, O[u][0][2] * g, O[u][1][0] * ge, O[u][1][2] * g);
             const float4 o1 = make_float4(O[u][0][1] * ge, O[u][0][3] * g, O[u][1][1] * ge, O[u][1][3] * g);
             const int col = 32 * u + 4 * gid;
-            if (team) {
+            if (team()) {
                 *reinterpret_cast<float4*>(&s.merge[warp][2 * tig][col]) = o0;
                 *reinterpret_cast<float4*>(&s.merge[warp][2 * tig + 1][col]) = o1;
             } else if (it.parts == 1) {
@@ -773,7 +812,7 @@ const uint32_t w0 = pack_f16x2(yy[0], yy[1]), w1 = pack_f16x2(yy[2], yy[3]);
                 if (2 * tig + 1 < a.G) __stcg(reinterpret_cast<float4*>(po + D), o1);
             }
         }
-        if (team) {
+        if (team()) {
             __syncthreads();
             const int col = tid % (D / 4) * 4, h = tid / (D / 4);  // thread -> 4 columns of one head
             if (h < a.G) {
@@ -801,7 +840,7 @@ const uint32_t w0 = pack_f16x2(yy[0], yy[1]), w1 = pack_f16x2(yy[2], yy[3]);
             }
         }
         if (it.parts > 1) {
-            if (!team && gid == 0) {
+            if (!team() && gid == 0) {
                 __stcg(a.part_ml + part * kMaxGroup + 2 * tig, make_float2(M0, l0));
                 __stcg(a.part_ml + part * kMaxGroup + 2 * tig + 1, make_float2(M1, l1));
             }
@@ -811,20 +850,20 @@ const uint32_t w0 = pack_f16x2(yy[0], yy[1]), w1 = pack_f16x2(yy[2], yy[3]);
     }
     if (pending) {  // (all warps of a team have the same)
         __threadfence();
-        if (team) __syncthreads(); else __syncwarp();
+        if (team()) __syncthreads(); else __syncwarp();
         int last = 0;
-        if ((team ? tid : lane) < pending) {
+        if ((team() ? tid : lane) < pending) {
             const Item& it = s.pending[warp][lane];
             last = atomicAdd(a.arrived + it.slot, 1) == it.parts - 1;
             if (last) a.arrived[it.slot] = 0;
-            if (team) s.last[lane] = last;
+            if (team()) s.last[lane] = last;
         }
-        if (team) __syncthreads();
+        if (team()) __syncthreads();
         __threadfence();
         for (int i = 0; i < pending; ++i)
-            if (team ? s.last[i] : __shfl_sync(0xffffffffu, last, i)) {
+            if (team() ? s.last[i] : __shfl_sync(0xffffffffu, last, i)) {
                 const Item& it = s.pending[warp][i];
-                if (team) {
+                if (team()) {
                     if (2 * warp < a.G) join_parts<D, 2>(a, it, 2 * warp);
                 } else {
                     for (int h0 = 0; h0 < a.G; h0 += 4) join_parts<D, 4>(a, it, h0);

@@ -398,8 +398,8 @@ def _attend(nf, c, q, out, ws, status, scale=0.0, sm=0, stream=0, R=None):
 
 def _check_attention(c, q, got, scale=None, rows=None):
     """Against 64 bits, element by element. The output rounds once to bf16 (2^-8 of it); each weight rounds to
-    fp16 (2^-11), and again when scaled by V's scale. A score is an fp32 sum of q (code + 8) less one of 8 q: at most |q| times 15 + 8
-    scales a column. Its roundings, in units of 2^-23 of that: 2 for the tensor-core steps of a group and 1 for that of
+    fp16 (2^-11), and again when scaled by V's scale. A score is an fp32 sum of q (code + 8) less one of 8 q: at
+    most |q| times 15 + 8 scales a column. Its roundings, in units of 2^-23 of that: 2 for the tensor-core steps of a group and 1 for that of
     the biases, 5 for the 10 additions of a group's bias, 1/2 for its split in three terms, 2 for 4 joins of groups:
     less than 11. (A scale is a seventh of its group's largest value or less; the bound takes the value itself for it,
     for steps of the tensor core that lose more.) A weight's relative error is twice (numerator, sum) that of its
@@ -424,7 +424,8 @@ def _check_attention(c, q, got, scale=None, rows=None):
             x_err = 11 * 2.0 ** -23 * sc * (np.abs(qq) @ (23 * unit).T).max(-1)
             bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -10 + 2 * x_err[:, None] + 2.0 ** -21) * mass
             # (some code of a group of 32 is not 0: its largest value is at least its scale)
-            bound += (2.0 ** -14 + (2.0 ** -26 + 2.0 ** -29) * len(V[h])) * np.abs(V[h]).max(0).reshape(-1, 32).max(-1).repeat(32)
+            largest = np.abs(V[h]).max(0).reshape(-1, 32).max(-1).repeat(32)
+            bound += (2.0 ** -14 + (2.0 ** -26 + 2.0 ** -29) * len(V[h])) * largest
             err = np.abs(gh[r, h * G:(h + 1) * G] - want)
             assert (err <= bound * (1 + 2.0 ** -6)).all(), (r, h, float((err / bound).max()))
             num, den = num + (err ** 2).sum(), den + (want ** 2).sum()
@@ -438,7 +439,9 @@ SHAPES = [  # lengths, nq, nkv, d
     ([1], 1, 1, 64), ([1, 2, 15, 16, 17, 0, 31, 32, 33], 4, 2, 64), ([0, 0, 5], 8, 8, 128),
     ([64, 100, 1], 32, 8, 128), ([257, 3, 640, 0, 17], 15, 5, 128), ([1000] * 3, 14, 2, 64), ([500, 700], 24, 4, 128),
     (list(range(0, 75)), 6, 1, 128), ([5000], 8, 1, 128), ([4096, 1, 3000], 64, 8, 128), ([20011], 7, 1, 64),
-    ([333] * 40, 32, 8, 128), ([9] * 700, 2, 2, 64)]
+    ([333] * 40, 32, 8, 128), ([9] * 700, 2, 2, 64),
+    # fewer (request, KV head) pairs than SMs, of equal lengths and of very different ones
+    ([300 + i for i in range(18)], 8, 8, 128), ([9000] + [3] * 16 + [0], 16, 8, 128), ([2000, 1, 40] * 5, 18, 9, 64)]
 
 
 @pytest.mark.parametrize("lens,nq,nkv,d", SHAPES, ids=lambda x: str(x)[:20] if isinstance(x, list) else str(x))

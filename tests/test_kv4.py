@@ -65,7 +65,8 @@ def test_memory_of_no_device_is_refused(call):
     (dict(T=-1), BAD), (dict(nq=-1), BAD), (dict(nkv=-1), BAD), (dict(d=127), BAD), (dict(rot=63), BAD),
     (dict(rot=0), BAD), (dict(rot=130), BAD), (dict(inter=2), BAD), (dict(idt=2), BAD), (dict(odt=-1), BAD),
     (dict(qs=511), BAD), (dict(kos=255), BAD), (dict(q=P + 1), BAD), (dict(ko=P * 4 + 2, odt=1), BAD),
-    (dict(pos=P * 5 + 2), BAD), (dict(freq=P * 6 + 4), BAD), (dict(scale=math.nan), BAD), (dict(qo=P, qos=520), BAD), (dict(ko=P * 3, odt=1), BAD),
+    (dict(pos=P * 5 + 2), BAD), (dict(freq=P * 6 + 4), BAD), (dict(scale=math.nan), BAD),
+    (dict(qo=P, qos=520), BAD), (dict(ko=P * 3, odt=1), BAD),
     (dict(d=514, rot=2, qs=4096, qos=4096, ks=4096, kos=4096), UNSUP), (dict(T=0), 0),
     (dict(nq=0, nkv=0, q=0, k=0, qo=0, ko=0), 0)])
 def test_rope_refusals(kw, want):
@@ -91,7 +92,8 @@ def test_row_refusals(read, kw, want):
     (dict(d=96), UNSUP), (dict(nq=18, qs=4096, os=4096), UNSUP), (dict(scale=-1.0), BAD), (dict(scale=math.nan), BAD),
     (dict(scale=math.inf), BAD), (dict(scale=3e38), BAD), (dict(pages=(1 << 30) + 1, nkv=2), BAD),
     (dict(pages=1 << 26, nkv=32, nq=32, qs=4096, os=4096, size=1 << 30), BAD), (dict(kv=P * 4 + 1), BAD),
-    (dict(ip=P * 5 + 2), BAD), (dict(ix=P * 6 + 2), BAD), (dict(status=P * 8 + 2), BAD), (dict(qs=1016), BAD), (dict(os=1028), BAD), (dict(q=P + 8), BAD),
+    (dict(ip=P * 5 + 2), BAD), (dict(ix=P * 6 + 2), BAD), (dict(status=P * 8 + 2), BAD),
+    (dict(qs=1016), BAD), (dict(os=1028), BAD), (dict(q=P + 8), BAD),
     (dict(out=P * 2 + 8), BAD), (dict(pool=P * 3 + 8), BAD), (dict(ws=P * 7 + 128), BAD), (dict(size=16), BAD),
     (dict(sm=-1), BAD), (dict(R=0), 0)])
 def test_attention_refusals(kw, want):
