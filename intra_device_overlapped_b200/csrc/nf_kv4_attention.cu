@@ -14,12 +14,12 @@ namespace nf {
 namespace {
 
 constexpr int kMaxGroup = 8;               // query heads per KV head: the N = 8 columns of the tensor instruction
-constexpr int kWarps = 12;                 // one CTA per SM, 168 registers a thread (16 warps of 128 spill)
+constexpr int kWarps = 16;                 // one CTA per SM, 128 registers a thread
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;                 // pairs of tiles in flight per warp
 constexpr int kMaxCtas = 160;              // sizes the workspace (a B200 has 148 SMs)
 constexpr int kMinShare = 4;               // places of a worker at least (Deal)
-constexpr int kOverhead = 10;              // what beginning and ending a (request, head) costs, in pages
+constexpr int kOverhead = 8;              // what beginning and ending a (request, head) costs, in pages
 constexpr int kJoin = 64, kJoinPart = 6;   // what a join by a warp costs, and each of its parts, in pages of a CTA
 constexpr int kWeightBits = 5, kScaleBits = 5;  // (Output, below) their sum and the slack of 5 make P < 2^15
 constexpr int kMaxParts = 2 * kWarps * kMaxCtas;
@@ -74,8 +74,10 @@ struct Smem {
     static constexpr int kHead = 18 * D;            // K and V tile of a head
     static constexpr int kRow = D + 4;              // merge rows, padded against bank conflicts
     alignas(128) uint8_t ring[kWarps][kStages][2 * kHead];
+    // rows of a team's warp: in the memory of its ring, which has done by then
+    __device__ __forceinline__ float* merge(int warp, int h) { return reinterpret_cast<float*>(ring[warp][0]) + h * kRow; }
     alignas(16) uint16_t q[kWarps][2][kMaxGroup * D];
-    float merge[kWarps][kMaxGroup][kRow];
+    uint4 bias[kWarps][32];  // a lane's two bias operands, its heads' factors of scores
     Item item[kWarps][2], pending[kWarps][2];
     float2 ml[kWarps][kMaxGroup];
     int64_t scan[kWarps], start[kThreads + 1];
@@ -237,7 +239,7 @@ __device__ __noinline__ bool find_item(const Kv4AttnArgs& a, Smem<D>& s, Item* o
     Item it;
     it.r = -1;
     int64_t next = stop;
-    // the thread's stretch of requests that holds the place, by 32 and 12 of their starts; then the request
+    // the thread's stretch of requests that holds the place, by 32 and then kSub of their starts; then the request
     constexpr int kSub = kThreads / 32;
     int span = (__popc(__ballot_sync(0xffffffffu, s.start[lane * kSub] <= pos)) - 1) * kSub;
     span += __popc(__ballot_sync(0xffffffffu, lane < kSub && s.start[span + min(lane, kSub - 1)] <= pos)) - 1;
@@ -391,10 +393,11 @@ __device__ __noinline__ void join_parts(const Kv4AttnArgs& a, const Item& it, in
 // Parts of one pair meet in the workspace; a worker reports its parts, two at most, when its share is done, and whoever
 // brings the last one joins them, in order.
 //
-// Measured, calls back to back: 512 requests of 1024 to 1536 keys, 32 query and 8 KV heads of 128: 152 us, 0.76 of a copy
-// of the 761 MB; of 1 to 2048 keys 101 us (0.67); 2 of 131072 keys with 64 query heads 68 us (0.66). What bounds it is
-// the turning of codes into operands: about 290 instructions a tile, 58 % of the issue slots and half of the logic pipe in
-// use, with the 3 warps a scheduler that 168 registers allow to cover latencies (16 warps of 128 registers spill).
+// Measured, calls back to back: 512 requests of 1024 to 1536 keys, 32 query and 8 KV heads of 128: 148 us, 0.79 of a copy
+// of the 761 MB; of 1 to 2048 keys 98 us (0.69); 2 of 131072 keys with 64 query heads 67 us (0.66). What bounds it is the
+// turning of codes into operands: about 300 instructions a tile, 60 % of the issue slots and 53 % of the logic pipe in
+// use, with 4 warps a scheduler to cover latencies. To fit 128 registers q's operands are read from shared memory again for
+// every tile; 12 warps of 168 registers hold them and take 153 us.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid_constant__ Kv4AttnArgs a) {
     constexpr int NG = D / 32, NW = NG / 2;
@@ -552,8 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
             __syncwarp();
             // q of head gid, columns 32 j + 8 t .. + 7, as fp16 times 2^(10 - e), 2^e the row's largest; pairs of even
             // nibbles times 16 more
-            uint32_t qf[NG][4], bias0, bias1;
-            float hs0, hs1;
+            uint4* const qf = reinterpret_cast<uint4*>(s.q[warp][k & 1]) + lane;  // in the memory of q
             {
                 float sum[NG];
 #pragma unroll
@@ -568,6 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
 #pragma unroll
                     for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, w[i] >> 16 & 0x7FFFu));
                 }
+                __syncwarp();  // all have read their q
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // exponent field; rows of zeros or subnormals count as 1, infinities and NaN as 254
@@ -579,18 +582,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                 // 2^107 and more) scores that differ do so by 2^20 and more, with the limit as without.
                 const float hs = fminf(fmaxf(a.scale_log2 * __int_as_float((127 - up0) << 23) *
                                                  __int_as_float((127 - up1) << 23) * 0x1p20f, 0x1p-140f), 0x1p127f);
-                hs0 = __shfl_sync(0xffffffffu, hs, 8 * tig);
-                hs1 = __shfl_sync(0xffffffffu, hs, 8 * tig + 4);
+                const float hs0 = __shfl_sync(0xffffffffu, hs, 8 * tig), hs1 = __shfl_sync(0xffffffffu, hs, 8 * tig + 4);
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
                     const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+                    uint32_t v[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float m = i % 2 ? m1 : m1 * 16.f;
-                        qf[j][i] = pack_f16x2(lo_bf16(w[i]) * m0 * m, hi_bf16(w[i]) * m0 * m);
-                        const __half2 back = *reinterpret_cast<__half2*>(&qf[j][i]);
+                        v[i] = pack_f16x2(lo_bf16(w[i]) * m0 * m, hi_bf16(w[i]) * m0 * m);
+                        const __half2 back = *reinterpret_cast<__half2*>(&v[i]);
                         sum[j] -= (__low2float(back) + __high2float(back)) * (i % 2 ? 0x1p-17f : 0x1p-21f);
                     }
+                    qf[32 * j] = make_uint4(v[0], v[1], v[2], v[3]);
                     sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
                     sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
                 }
@@ -607,8 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                     }
                     return w;
                 };
-                bias0 = term(sum[0], sum[1]);
-                bias1 = NW == 2 ? term(sum[NG - 2], sum[NG - 1]) : 0;
+                s.bias[warp][lane] = make_uint4(term(sum[0], sum[1]), NW == 2 ? term(sum[NG - 2], sum[NG - 1]) : 0,
+                                                __float_as_uint(hs0), __float_as_uint(hs1));
             }
             for (int left = keys - offset() * kKv4Slots; left > 0; left -= step * kKv4Slots) {  // keys from the pair on
                 if (flying < kStages) fill(k);  // (a new stretch to begin)
@@ -631,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                     for (int e = 0; e < 4; ++e) yy[e] = ex2_approx(yy[e]);
                     l0 += yy[0] + yy[2];
                     l1 += yy[1] + yy[3];
-const uint32_t w0 = pack_f16x2(yy[0], yy[1]), w1 = pack_f16x2(yy[2], yy[3]);
+                    const uint32_t w0 = pack_f16x2(yy[0], yy[1]), w1 = pack_f16x2(yy[2], yy[3]);
 #pragma unroll
                     for (int u = 0; u < NW; ++u) {
                         const uint32_t pa = scales_f16(tta[u], f[u]), pb = scales_f16(ttb[u], f[u]);
@@ -649,6 +653,7 @@ const uint32_t w0 = pack_f16x2(yy[0], yy[1]), w1 = pack_f16x2(yy[2], yy[3]);
                 };
                 if (none != 3u) {
                     float x[2][4];
+                    const uint2 bias = *reinterpret_cast<const uint2*>(&s.bias[warp][lane]);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint8_t* kt = tile + i * S::kHead;
@@ -657,7 +662,7 @@ const uint32_t w0 = pack_f16x2(yy[0], yy[1]), w1 = pack_f16x2(yy[2], yy[3]);
                         load_words<NG>(kt + 4 * D + lane * (D / 8), kb);    // slot gid + 8
                         load_scales<NG>(kt + 8 * D + gid * (2 * NG), sa);
                         load_scales<NG>(kt + 8 * D + (gid + 8) * (2 * NG), sb);
-                        mma_bf16(x[i], sa[0], sb[0], sa[NW - 1], sb[NW - 1], bias0, bias1);
+                        mma_bf16(x[i], sa[0], sb[0], sa[NW - 1], sb[NW - 1], bias.x, bias.y);
 #pragma unroll
                         for (int j = 0; j < NG; ++j) {
                             uint32_t ea[4], eb[4];
@@ -666,8 +671,9 @@ const uint32_t w0 = pack_f16x2(yy[0], yy[1]), w1 = pack_f16x2(yy[2], yy[3]);
                             const uint32_t a0[4] = {ea[0], eb[0], ea[1], eb[1]}, a1[4] = {ea[2], eb[2], ea[3], eb[3]};
                             const float zero[4] = {0.f, 0.f, 0.f, 0.f};
                             float acc[4];
-                            mma_f16(acc, a0, qf[j][0], qf[j][1], zero);
-                            mma_f16(acc, a1, qf[j][2], qf[j][3], acc);
+                            const uint4 qv = qf[32 * j];
+                            mma_f16(acc, a0, qv.x, qv.y, zero);
+                            mma_f16(acc, a1, qv.z, qv.w, acc);
                             const float ga = j % 2 ? hi_bf16(sa[j / 2]) : lo_bf16(sa[j / 2]);
                             const float gb = j % 2 ? hi_bf16(sb[j / 2]) : lo_bf16(sb[j / 2]);
                             x[i][0] = fmaf(ga, acc[0], x[i][0]);
@@ -676,6 +682,8 @@ const uint32_t w0 = pack_f16x2(yy[0], yy[1]), w1 = pack_f16x2(yy[2], yy[3]);
                             x[i][3] = fmaf(gb, acc[3], x[i][3]);
                         }
                     }
+                    const float2 hs = *reinterpret_cast<const float2*>(&s.bias[warp][lane].z);
+                    const float hs0 = hs.x, hs1 = hs.y;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint8_t* vt = tile + i * S::kHead + 17 * D;
@@ -801,8 +809,8 @@ const uint32_t w0 = pack_f16x2(yy[0], yy[1]), w1 = pack_f16x2(yy[2], yy[3]);
             const float4 o1 = make_float4(O[u][0][1] * ge, O[u][0][3] * g, O[u][1][1] * ge, O[u][1][3] * g);
             const int col = 32 * u + 4 * gid;
             if (team()) {
-                *reinterpret_cast<float4*>(&s.merge[warp][2 * tig][col]) = o0;
-                *reinterpret_cast<float4*>(&s.merge[warp][2 * tig + 1][col]) = o1;
+                *reinterpret_cast<float4*>(s.merge(warp, 2 * tig) + col) = o0;
+                *reinterpret_cast<float4*>(s.merge(warp, 2 * tig + 1) + col) = o1;
             } else if (it.parts == 1) {
                 if (2 * tig < a.G) store_out(a, it, D, 2 * tig, col, o0, l0);
                 if (2 * tig + 1 < a.G) store_out(a, it, D, 2 * tig + 1, col, o1, l1);
@@ -824,7 +832,7 @@ const uint32_t w0 = pack_f16x2(yy[0], yy[1]), w1 = pack_f16x2(yy[2], yy[3]);
                 for (int w = 0; w < kWarps; ++w) {
                     const float2 ml = s.ml[w][h];
                     const float c = part_factor(ml.x, M);
-                    const float4 v = *reinterpret_cast<const float4*>(&s.merge[w][h][col]);
+                    const float4 v = *reinterpret_cast<const float4*>(s.merge(w, h) + col);
                     L += c * ml.y;
                     o.x += c * v.x;
                     o.y += c * v.y;
