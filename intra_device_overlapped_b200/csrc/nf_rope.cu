@@ -41,26 +41,24 @@ __device__ __forceinline__ void form_turns(const RopeArgs& a, int t, float2* cs,
     }
 }
 
-// (x, y) at angle p f: (x c - y s, y c + x s). A token's turns are formed once, in shared memory, for all its heads; a
-// thread then takes 8 pairs of a head, two vectors of 8 columns in (16 bytes in bf16) and out. Every value is read and
-// written once, so the kernel is bound by HBM: 8192 rows of 72 bf16 heads of 128 take 55 us, 0.83 of a copy. With 4 tokens a
-// block (kTokens) all threads have turns to form; with few tokens more blocks count for more. 8192 such rows 55 us (62 with
-// one token a block), 2048 14.4 (16), 1024 8.5 (8.7), 512 6.6 (5.2), 32 6.3 (3.1).
-template <typename TI, typename TO, int kTokens>
-__global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const RopeArgs a, const FastDiv per_token,
-                                                                const FastDiv per_head) {
-    __shared__ float2 cs[kTokens][kRopeMaxDim / 2];
-    const int t0 = blockIdx.x * kTokens, tokens = min(kTokens, a.T - t0), half = a.rot / 2;
-    constexpr int kShare = kRopeThreads / kTokens;
-    if ((int)threadIdx.x / kShare < tokens)
-        form_turns(a, t0 + threadIdx.x / kShare, cs[threadIdx.x / kShare], threadIdx.x % kShare, kShare);
+// (x, y) at angle p f: (x c - y s, y c + x s). A block takes a token, whose turns are formed once, in shared memory, for all
+// its heads; a thread takes 8 pairs of a head at a time, two vectors of 8 columns in (16 bytes in bf16) and out. Every value
+// is read and written once, so the kernel is bound by HBM: 8192 rows of 72 bf16 heads of 128 take 50.7 us, 0.91 of a copy,
+// 8192 of 40 heads from fp32 to bf16 40.1, 0.96. Blocks of 256 threads end soonest where each has an SM nearly for itself,
+// small ones keep more loads in flight and more tokens' turns beside them: with 256, 128 and 64 threads 32 such rows 3.2, 3.9
+// and 5.6 us, 512 5.3, 5.3 and 6.6, 1024 8.5, 7.6 and 8.2, 2048 16, 14.8 and 13.2. (Two vectors a thread at a time: 10 %
+// more time, for the registers that they hold.)
+template <typename TI, typename TO>
+__global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const RopeArgs a, const FastDiv per_head) {
+    __shared__ float2 cs[kRopeMaxDim / 2];
+    const int64_t t = blockIdx.x;
+    const int half = a.rot / 2, turned = a.rot / 16, units = (a.q.heads + a.k.heads) * per_head.d;
+    form_turns(a, (int)t, cs, threadIdx.x, blockDim.x);
     __syncthreads();
-    const int units = tokens * per_token.d, turned = a.rot / 16;
-#pragma unroll 2
-    for (int e = threadIdx.x; e < units; e += kRopeThreads) {
-        const int tt = per_token(e), r = e - tt * per_token.d;
-        int h = per_head(r);
-        const int u = r - h * per_head.d;
+#pragma unroll 1
+    for (int e = threadIdx.x; e < units; e += blockDim.x) {
+        int h = per_head(e);
+        const int u = e - h * per_head.d;
         const bool isq = h < a.q.heads;
         const RopeSide& side = isq ? a.q : a.k;
         h -= isq ? 0 : a.q.heads;
@@ -71,8 +69,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const RopeArgs a
             j = i + half;
         }
         if (u >= turned && !a.copy) continue;
-        const TI* x = static_cast<const TI*>(side.in) + (t0 + tt) * side.in_stride + (int64_t)h * a.d;
-        TO* y = static_cast<TO*>(side.out) + (t0 + tt) * side.out_stride + (int64_t)h * a.d;
+        const TI* x = static_cast<const TI*>(side.in) + t * side.in_stride + (int64_t)h * a.d;
+        TO* y = static_cast<TO*>(side.out) + t * side.out_stride + (int64_t)h * a.d;
         float p[8], q[8];
         load_row8(x + i, p);
         load_row8(x + j, q);
@@ -80,7 +78,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const RopeArgs a
             if (a.interleaved) {
 #pragma unroll
                 for (int n = 0; n < 8; n += 2) {
-                    const float2 w = cs[tt][8 * u + n / 2], z = cs[tt][8 * u + 4 + n / 2];
+                    const float2 w = cs[8 * u + n / 2], z = cs[8 * u + 4 + n / 2];
                     const float p0 = p[n], q0 = q[n];
                     p[n] = p0 * w.x - p[n + 1] * w.y;
                     p[n + 1] = p[n + 1] * w.x + p0 * w.y;
@@ -90,7 +88,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const RopeArgs a
             } else {
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
-                    const float2 w = cs[tt][8 * u + n];
+                    const float2 w = cs[8 * u + n];
                     const float p0 = p[n];
                     p[n] = p0 * w.x - q[n] * w.y;
                     q[n] = q[n] * w.x + p0 * w.y;
@@ -148,13 +146,8 @@ bool side_vec(const RopeSide& s) {
 
 template <typename TI, typename TO>
 cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
-    const int heads = a.q.heads + a.k.heads;
     if (a.d % 16 == 0 && a.rot % 16 == 0 && side_vec<TI, TO>(a.q) && side_vec<TI, TO>(a.k)) {
-        const FastDiv per_token(heads * (a.d / 16)), per_head(a.d / 16);
-        if (a.T < 1024)
-            rope_vec_kernel<TI, TO, 1><<<a.T, kRopeThreads, 0, s>>>(a, per_token, per_head);
-        else
-            rope_vec_kernel<TI, TO, 4><<<(a.T - 1) / 4 + 1, kRopeThreads, 0, s>>>(a, per_token, per_head);
+        rope_vec_kernel<TI, TO><<<a.T, a.T < 768 ? 256 : a.T < 1536 ? 128 : 64, 0, s>>>(a, FastDiv(a.d / 16));
     } else {
         const int grid = a.T < 148 * 8 ? a.T : 148 * 8;
         rope_kernel<TI, TO><<<grid, kRopeThreads, 0, s>>>(a);
