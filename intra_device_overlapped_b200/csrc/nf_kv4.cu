@@ -9,8 +9,8 @@
 namespace nf {
 namespace {
 
-constexpr int kRowThreads = 256;
-constexpr int kUnroll = 4;  // heads of a lane, in flight together
+constexpr int kRowThreads = 128;  // append of fp32 rows: with 256 6 % slower, with 512 18 %
+constexpr int kUnroll = 4;  // heads of a lane, in flight together: append of 8192 rows is fastest so (with 2 6 % slower, with 8 26 %)
 constexpr float kLargest = 0x1p60f, kSmallest = 0x1p-60f;
 
 struct Kv4RowArgs {
@@ -59,34 +59,28 @@ struct Task {
 };
 
 // Codes of 8 values in units of s, code + 8 of x[e] in nibble e: the exact quotients x / s rounded half to even.
-// 1.5 * 2^23 + x inv, inv within 2^-22 of 1 / s, rounds to an integer k in its last bits (no conversion instruction:
-// those run at a quarter of the rate); it is the right one or, next to a border, its neighbour. The remainder x - k s has
-// at most 24 bits there (|x - k s| <= s and x is no finer than 2^-24 s where k != 0), so the fma gives it exactly: a
-// magnitude below s / 2 is settled, and else (in one of twenty warps) its double against s, the tie going to even,
-// tells. |x| <= 7.04 s: no code leaves -7..7.
+// q = x inv, inv within 2^-23 of 1 / s, and its remainder x - q s, exact by the fma, give the quotient as nearest fp32
+// number but for 2^-45. A quotient half way between integers is such a number. Another one is more than half a step of
+// fp32 away from it (x lies on a grid no finer than its own steps, and s has 8 bits), so it is not taken for it. Adding
+// 1.5 * 2^23 then rounds to an integer in the last bits (no conversion instruction: those run at a quarter of the rate).
+// |x| <= 7.04 s: no code leaves -7..7.
 __device__ __forceinline__ uint32_t codes_of(const float* x, float s, float inv) {
     constexpr float kMagic = 12582912.f;
     // the sum of 16^e (0x4B400000 + k_e), and what makes it the sum of 16^e (8 + k_e), in 32 bits
-    constexpr uint32_t kStart = 0x88888888u - 0x4B400000u * 0x11111111u;
-    uint32_t codes = kStart;
-    float worst = 0.f;
+    uint32_t codes = 0x88888888u - 0x4B400000u * 0x11111111u;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float t = fmaf(x[e], inv, kMagic);
-        worst = fmaxf(worst, fabsf(fmaf(kMagic - t, s, x[e])));
-        codes += __float_as_uint(t) << (4 * e);
-    }
-    if (worst + worst >= s) {
-        codes = kStart;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float t = fmaf(x[e], inv, kMagic), r = fmaf(kMagic - t, s, x[e]);
-            int k = __float_as_int(t);
-            if (__float_as_int(fabsf(r) + fabsf(r)) + (k & 1) > __float_as_int(s)) k += 1 | (__float_as_int(r) >> 31);
-            codes += (uint32_t)k << (4 * e);
-        }
+        const float q = x[e] * inv;
+        codes += __float_as_uint(fmaf(fmaf(-q, s, x[e]), inv, q) + kMagic) << (4 * e);
     }
     return codes;
+}
+
+// The larger, NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
 // Nibble 2 p + h of a word to nibble p of half h, and back
@@ -106,8 +100,8 @@ __device__ __forceinline__ uint32_t shuffle_nibbles(uint32_t x) {
 // Append. A group's largest magnitude is found by 4 lanes, its scale by each of them; a K row's codes are written as 4-byte
 // words of 64 (32) consecutive bytes, a V row's as 2-byte units of 4 (2) sectors that two neighbouring slots share and L2
 // joins. All of a lane's rows are loaded before the first is quantised, and before its token's slot is known. 8192
-// rows of 8 heads of 128 take 13.5 us in bf16 (42 MB read, 9.4 written: 6.6 at a copy's rate), 13.8 in fp32 (11.7): bound
-// by instruction issue, 73 % of the slots, of which the rounding takes a third.
+// rows of 8 heads of 128 take 10.6 us in bf16 (34 MB read, 9.4 written: 6.6 at a copy's rate), 12.8 in fp32 (11.7), 32768
+// in bf16 38 (26): bound by instruction issue, of which the rounding takes a third.
 template <int D, typename TK, typename TV>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowArgs a) {
     using W = Task<D>;
@@ -134,14 +128,14 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowArg
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-        // largest magnitude of the group by its bits: ordered like the values, NaN above infinity
-        uint32_t top = 0;
+        // largest magnitude of the group, NaN above all
+        float big = fabsf(x[i][0]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[i][e]) & 0x7fffffffu);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float big = __uint_as_float(top);
-        const float ab = big <= kLargest * 2.f ? bf2f(f2bf(big)) : big;
+        for (int e = 1; e < 8; ++e) big = max_nan(big, fabsf(x[i][e]));
+        big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        float ab = big;
+        if constexpr (sizeof(TK) == 4 || sizeof(TV) == 4) ab = big <= kLargest * 2.f ? bf2f(f2bf(big)) : big;
         uint16_t sbits = 0;
         uint32_t codes = 0x88888888u;  // code of column 8 m + e in nibble e
         if (!(ab <= kLargest)) {
