@@ -599,7 +599,8 @@ int64_t nf_kv4_workspace_bytes(int32_t n_q_heads, int32_t n_kv_heads, int32_t he
  * out[r][h] = softmax(softmax_scale * q[r][h] K_r^T) V_r over the first kv_len[r] keys of request r (the new
  * token's among them once it has been appended), K and V of head h / (n_q_heads / n_kv_heads); zeros where
  * kv_len[r] is 0.
- *   q, out         bf16 rows [n_q_heads x head_dim], 16-byte aligned, strides multiples of 8 elements
+ *   q, out         bf16 rows [n_q_heads x head_dim], 16-byte aligned, strides multiples of 8 elements; out may be q
+ *                  itself (same stride; other overlaps are not allowed)
  *   kv_len         device int32 [num_requests]; page_indptr, page_indices: CSR page table
  *   softmax_scale  0: 1 / sqrt(head_dim); NF_ERR_INVALID_ARGUMENT when negative or, times log2(e), not finite
  *   workspace      nf_kv4_workspace_bytes bytes, 256-byte aligned, zeroed by the caller once before its first

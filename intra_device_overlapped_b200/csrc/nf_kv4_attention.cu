@@ -935,6 +935,7 @@ extern "C" nf_status nf_op_kv4_decode_attention(const void* q, int64_t q_stride,
     const double scale = softmax_scale != 0.f ? (double)softmax_scale : 1.0 / std::sqrt((double)head_dim);
     const float scale_log2 = (float)(scale * 1.4426950408889634);
     if (!(scale > 0.0) || !std::isfinite(scale_log2)) return NF_ERR_INVALID_ARGUMENT;
+    if (q == out && q_stride != out_stride) return NF_ERR_INVALID_ARGUMENT;
     if (q_stride < row || out_stride < row || q_stride % 8 || out_stride % 8 || !nf::aligned(q, 16) ||
         !nf::aligned(out, 16) || !nf::aligned(pool, 16) || !nf::aligned(workspace, 256) ||
         workspace_bytes < nf_kv4_workspace_bytes(n_q_heads, n_kv_heads, head_dim))

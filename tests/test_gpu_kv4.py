@@ -399,8 +399,8 @@ def _attend(nf, c, q, out, ws, status, scale=0.0, sm=0, stream=0, R=None):
 def _check_attention(c, q, got, scale=None, rows=None):
     """Against 64 bits, element by element. The output rounds once to bf16 (2^-8 of it); each weight rounds to
     fp16 (2^-11), and again when scaled by V's scale. A score is an fp32 sum of q (code + 8) less one of 8 q: at
-    most |q| times 15 + 8 scales a column. Its roundings, in units of 2^-23 of that: 2 for the tensor-core steps of a group and 1 for that of
-    the biases, 5 for the 10 additions of a group's bias, 1/2 for its split in three terms, 2 for 4 joins of groups:
+    most |q| times 15 + 8 scales a column. Its roundings, in units of 2^-23 of that: 2 for the tensor-core steps of a
+    group and 1 for that of the biases, 5 for the 10 additions of a group's bias, 1/2 for its split in three terms, 2 for 4 joins of groups:
     less than 11. (A scale is a seventh of its group's largest value or less; the bound takes the value itself for it,
     for steps of the tensor core that lose more.) A weight's relative error is twice (numerator, sum) that of its
     exponent; ex2 adds 2^-22 and the sums 2^-22 more. With S the group's largest scale so far, f in [2^3, 2^5) / S and
@@ -467,6 +467,9 @@ def test_attention(nf, lens, nq, nkv, d):
         if sm == 0:
             assert torch.equal(out, first)
         _check_attention(c, q, out, rows=range(min(R, 12)))
+    _attend(nf, c, q, q, ws, status)   # in place
+    torch.cuda.synchronize()
+    assert torch.equal(q, first)
 
 
 @pytest.mark.parametrize("scale,spread", [(0.02, 1.0), (1.0, 1.0), (3.0, 4.0)])

@@ -90,7 +90,7 @@ def test_row_refusals(read, kw, want):
     (dict(ws=0), BAD), (dict(status=0), BAD), (dict(pages=0), BAD), (dict(R=-1), BAD),
     (dict(R=nf.NF_KV4_MAX_REQUESTS + 1), BAD), (dict(nq=0), BAD), (dict(nq=9), BAD), (dict(nkv=0), BAD),
     (dict(d=96), UNSUP), (dict(nq=18, qs=4096, os=4096), UNSUP), (dict(scale=-1.0), BAD), (dict(scale=math.nan), BAD),
-    (dict(scale=math.inf), BAD), (dict(scale=3e38), BAD), (dict(pages=(1 << 30) + 1, nkv=2), BAD),
+    (dict(scale=math.inf), BAD), (dict(out=P, os=1032), BAD), (dict(scale=3e38), BAD), (dict(pages=(1 << 30) + 1, nkv=2), BAD),
     (dict(pages=1 << 26, nkv=32, nq=32, qs=4096, os=4096, size=1 << 30), BAD), (dict(kv=P * 4 + 1), BAD),
     (dict(ip=P * 5 + 2), BAD), (dict(ix=P * 6 + 2), BAD), (dict(status=P * 8 + 2), BAD),
     (dict(qs=1016), BAD), (dict(os=1028), BAD), (dict(q=P + 8), BAD),
