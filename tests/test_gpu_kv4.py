@@ -645,6 +645,24 @@ def test_attention_ordinary_length_row_among_many_empty(nf):
     assert (out == 0).all()
 
 
+@pytest.mark.parametrize("R,nq,nkv", [(16384, 2, 1), (16383, 1, 1), (3, 2048, 256), (150, 256, 256)])
+def test_attention_at_the_limits(nf, R, nq, nkv):
+    """The most requests and the most heads that a call takes."""
+    rng = np.random.default_rng(R + nkv)
+    lens = rng.integers(0, 41, R)
+    lens[-1] = 700 if R < 100 else 90
+    c = Cache([int(n) for n in lens], nkv, 64, seed=R)
+    q = _dev(rng.standard_normal((R, nq, 64)).astype(np.float32), torch.bfloat16)
+    out, ws, status = torch.full_like(q, float("nan")), _workspace(nf, nq, nkv, 64), _status()
+    _attend(nf, c, q, out, ws, status)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    rows = [0, R - 1] if R < 200 else [0, R - 1, *rng.integers(0, R, 300)]
+    _check_attention(c, q, out, rows=rows)
+    gone = torch.from_numpy(lens == 0).to(DEV)
+    assert (out[gone] == 0).all() and out[~gone].isfinite().all()
+
+
 # --- together ---------------------------------------------------------------------------------------
 
 
