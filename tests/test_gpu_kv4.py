@@ -834,6 +834,14 @@ def test_calls_from_two_streams_at_once(nf):
         _check_attention(caches[i], q[i], outs[i])
 
 
+@pytest.mark.parametrize("op,extra", [("kv4_decode_attention", []), ("kv4_decode_attention", ["--requests", "3", "--sm", "2"]),
+                                      ("kv4_append", []), ("kv4_read", ["--rows", "9"]), ("rope", []), ("page_map", [])])
+def test_each_operation_timed_alone(nf, op, extra, capsys):
+    from intra_device_overlapped_b200 import opbench
+    got = opbench.main(["--op", op, "--workload", "tiny_layer", "--reps", "2", *extra])
+    assert got["us"] > 0 and got["bytes"] > 0 and op in capsys.readouterr().out
+
+
 def test_host_memory_is_refused(nf):
     host = torch.zeros(1 << 16, dtype=torch.uint8).pin_memory()
     dev = torch.zeros(1 << 16, dtype=torch.uint8, device=DEV)
