@@ -86,9 +86,9 @@ struct Smem {
     int last[2];
 };
 
-// Pages that request r reads: its keys, cut to what its row of the page table holds.
-__device__ __forceinline__ int pages_of(const Kv4AttnArgs& a, int r, int* keys, bool report) {
-    const int p0 = a.indptr[r];
+// Pages that request r reads: its keys, cut to what its row of the page table holds; *at: where the row begins.
+__device__ __forceinline__ int pages_of(const Kv4AttnArgs& a, int r, int* keys, int* at, bool report) {
+    const int p0 = *at = a.indptr[r];
     int64_t np = (int64_t)a.indptr[r + 1] - p0;
     int n = a.kv_len[r];
     bool bad = n < 0 || p0 < 0 || np < 0;
@@ -246,8 +246,8 @@ __device__ __noinline__ bool find_item(const Kv4AttnArgs& a, Smem<D>& s, Item* o
     int64_t at = s.start[span];
     const int end = min(a.R, (span + 1) * per);
     for (int r = span * per; r < end; r += 32) {
-        int keys = 0, pages = 0;
-        if (r + lane < end) pages = pages_of(a, r + lane, &keys, false);
+        int keys = 0, pages = 0, row = 0;
+        if (r + lane < end) pages = pages_of(a, r + lane, &keys, &row, false);
         int64_t places = deal.places(pages);
         const int64_t upto = at + warp_prefix(places * a.nkv, lane);
         const uint32_t past = __ballot_sync(0xffffffffu, upto > pos);
@@ -255,6 +255,7 @@ __device__ __noinline__ bool find_item(const Kv4AttnArgs& a, Smem<D>& s, Item* o
             const int src = __ffs(past) - 1;
             pages = __shfl_sync(0xffffffffu, pages, src);
             keys = __shfl_sync(0xffffffffu, keys, src);
+            row = __shfl_sync(0xffffffffu, row, src);
             places = __shfl_sync(0xffffffffu, places, src);
             const int64_t begin = __shfl_sync(0xffffffffu, upto, src) - places * a.nkv;
             int h = -1;  // the last head that begins at or before pos
@@ -280,7 +281,7 @@ __device__ __noinline__ bool find_item(const Kv4AttnArgs& a, Smem<D>& s, Item* o
             if (b < e) {
                 it.r = r + src;
                 it.h = h;
-                it.first = a.indptr[it.r] + b;
+                it.first = row + b;
                 it.pages = e - b;
                 it.keys = min(keys - b * kKv4Slots, it.pages * kKv4Slots);
                 it.slot = 2 * (worker - it.c) + 1;
@@ -306,46 +307,58 @@ __device__ __forceinline__ void store_out(const Kv4AttnArgs& a, const Item& it, 
 }
 
 // Parts of a (request, head), joined in order into the output by one warp: heads h0 .. h0 + H - 1, 4 columns of a head
-// to a lane. The weights of 32 / H parts are formed by a lane each, so that the partial rows are all that the threads
-// wait for; their loads do not depend on one another.
+// to a lane. The weights of 32 / H parts are formed by a lane each; rows of 4 parts are loaded at a time, the first before
+// the maximum is known. One body for any number of parts (the last is loaded again, with weight 0, for those that are
+// missing): what a join costs is mostly code that no cache holds yet.
 template <int D, int H>
 __device__ __noinline__ void join_parts(const Kv4AttnArgs& a, const Item& it, int h0) {
     constexpr int kRows = 128 / D, kAtOnce = 32 / H;  // heads that the lanes cover at a time; parts a round
-    const int lane = threadIdx.x & 31, col = lane % (D / 4) * 4, row = lane / (D / 4);
+    static_assert(kAtOnce % 4 == 0, "rows of 4 parts at a time");
+    const int lane = threadIdx.x & 31, col = lane % (D / 4) * 4, row = lane / (D / 4), parts = it.parts;
     const float2* const ml = a.part_ml + h0 + lane % H;
-    float M = -INFINITY, L = 0.f;
-    for (int c = lane / H; c < it.parts; c += kAtOnce)
-        M = fmaxf(M, __ldcg(ml + (int64_t)part_slot(it, c) * kMaxGroup).x);
+    const float* const po = a.part_o + (int64_t)h0 * D + col;
+    const int last = a.G - 1 - h0;
+    auto weight_of = [&](int c) {
+        return c < parts ? __ldcg(ml + (int64_t)part_slot(it, c) * kMaxGroup) : make_float2(-INFINITY, 0.f);
+    };
+    float4 v[4][H / kRows], o[H / kRows];
+    auto load = [&](int c) {
 #pragma unroll
-    for (int o = H; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float4 o[H / kRows];
-    const float* po[H / kRows];
+        for (int p = 0; p < 4; ++p) {
+            const float* at = po + (int64_t)part_slot(it, min(c + p, parts - 1)) * a.G * D;
 #pragma unroll
-    for (int i = 0; i < H / kRows; ++i) {
-        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        po[i] = a.part_o + (int64_t)min(h0 + i * kRows + row, a.G - 1) * D + col;
-    }
-    for (int c0 = 0; c0 < it.parts; c0 += kAtOnce) {
-        float w = 0.f;
-        if (c0 + lane / H < it.parts) {
-            const float2 m = __ldcg(ml + (int64_t)part_slot(it, c0 + lane / H) * kMaxGroup);
-            w = part_factor(m.x, M);
+            for (int i = 0; i < H / kRows; ++i)
+                v[p][i] = __ldcg(reinterpret_cast<const float4*>(at + min(i * kRows + row, last) * D));
+        }
+    };
+    float2 m = weight_of(lane / H);
+    load(0);
+    float M = m.x, L = 0.f;
+#pragma unroll 1
+    for (int c = kAtOnce + lane / H; c < parts; c += kAtOnce) M = fmaxf(M, weight_of(c).x);
+#pragma unroll
+    for (int of = H; of < 32; of <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, of));
+#pragma unroll
+    for (int i = 0; i < H / kRows; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float w = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < parts; c += 4) {
+        if (c % kAtOnce == 0) {
+            if (c) m = weight_of(c + lane / H);
+            w = c + lane / H < parts ? part_factor(m.x, M) : 0.f;
             L += w * m.y;
         }
-        const int n = min(kAtOnce, it.parts - c0);
-#pragma unroll 4
-        for (int c = 0; c < n; ++c) {
-            const int64_t at = (int64_t)part_slot(it, c0 + c) * a.G * D;
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
 #pragma unroll
             for (int i = 0; i < H / kRows; ++i) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(po[i] + at));
-                const float f = __shfl_sync(0xffffffffu, w, H * c + i * kRows + row);
-                o[i].x += f * v.x;
-                o[i].y += f * v.y;
-                o[i].z += f * v.z;
-                o[i].w += f * v.w;
+                const float f = __shfl_sync(0xffffffffu, w, H * (c % kAtOnce + p) + i * kRows + row);
+                o[i].x += f * v[p][i].x;
+                o[i].y += f * v[p][i].y;
+                o[i].z += f * v[p][i].z;
+                o[i].w += f * v[p][i].w;
             }
-        }
+        if (c + 4 < parts) load(c + 4);
     }
 #pragma unroll
     for (int of = H; of < 32; of <<= 1) L += __shfl_xor_sync(0xffffffffu, L, of);
@@ -353,7 +366,7 @@ __device__ __noinline__ void join_parts(const Kv4AttnArgs& a, const Item& it, in
     for (int i = 0; i < H / kRows; ++i) {
         const int h = i * kRows + row;
         const float sum = __shfl_sync(0xffffffffu, L, h);
-        if (h0 + h < a.G) store_out(a, it, D, h0 + h, col, o[i], sum);
+        if (h <= last) store_out(a, it, D, h0 + h, col, o[i], sum);
     }
 }
 
@@ -413,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
         const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
         Deal d;
         d.chunk = 0;
-        int keys;
+        int keys, at;
         int64_t sum = 0, upto, before;
         auto scan = [&]() {
             upto = warp_prefix(sum * a.nkv, lane);
@@ -429,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
         };
         const int64_t pairs = (int64_t)a.R * a.nkv;
         if (pairs < gridDim.x) {  // (one request to a thread at most)
-            const int pages = r0 < r1 ? pages_of(a, r0, &keys, blockIdx.x == 0) : 0;
+            const int pages = r0 < r1 ? pages_of(a, r0, &keys, &at, blockIdx.x == 0) : 0;
             sum = pages;
             scan();
             const int n = (int)pairs, others = gridDim.x - n;
@@ -442,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                 d.chunk = 0;
             sum = d.places(pages);
         } else {
-            for (int r = r0; r < r1; ++r) sum += d.places(pages_of(a, r, &keys, blockIdx.x == 0));
+            for (int r = r0; r < r1; ++r) sum += d.places(pages_of(a, r, &keys, &at, blockIdx.x == 0));
         }
         scan();
         d.share = d.chunk ? 1 : max(divide(d.total + workers - 1, workers), (int64_t)kMinShare);
@@ -452,13 +465,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
             s.deal = d;
         }
         __syncthreads();
-    }
-    // requests without keys: zeros
-    for (int r = blockIdx.x; r < a.R; r += gridDim.x) {
-        int keys;
-        if (pages_of(a, r, &keys, false) == 0)
-            for (int i = tid * 8; i < a.nkv * a.G * D; i += kThreads * 8)
-                *reinterpret_cast<uint4*>(a.out + r * a.out_stride + i) = make_uint4(0, 0, 0, 0);
     }
     // (read again where it is used: the loop has no register for it)
     auto team = [&]() { return s.deal.chunk != 0; };
@@ -535,6 +541,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
 
     const int gid = lane >> 2, tig = lane & 3;
     int pending = 0;  // parts written, to be reported
+    fill(0);
+    // requests without keys: zeros
+    for (int r = blockIdx.x; r < a.R; r += gridDim.x) {
+        int keys, at;
+        if (pages_of(a, r, &keys, &at, false) == 0)
+            for (int i = tid * 8; i < a.nkv * a.G * D; i += kThreads * 8)
+                *reinterpret_cast<uint4*>(a.out + r * a.out_stride + i) = make_uint4(0, 0, 0, 0);
+    }
     for (int k = 0;; ++k) {
         if (flying < kStages) fill(k);
         if (k >= ahead) break;
