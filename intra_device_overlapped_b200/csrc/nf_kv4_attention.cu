@@ -407,7 +407,7 @@ __device__ __noinline__ void join_parts(const Kv4AttnArgs& a, const Item& it, in
 // brings the last one joins them, in order.
 //
 // Measured, calls back to back: 512 requests of 1024 to 1536 keys, 32 query and 8 KV heads of 128: 148 us, 0.79 of a copy
-// of the 761 MB; of 1 to 2048 keys 98 us (0.69); 2 of 131072 keys with 64 query heads 67 us (0.66). What bounds it is the
+// of the 761 MB; of 1 to 2048 keys 97.5 us (0.69); 2 of 131072 keys with 64 query heads 67 us (0.66). What bounds it is the
 // turning of codes into operands: about 300 instructions a tile, 60 % of the issue slots and 53 % of the logic pipe in
 // use, with 4 warps a scheduler to cover latencies. To fit 128 registers q's operands are read from shared memory again for
 // every tile; 12 warps of 168 registers hold them and take 153 us.
