@@ -21,7 +21,7 @@ constexpr int kMaxCtas = 160;              // sizes the workspace (a B200 has 14
 constexpr int kMinShare = 4;               // places of a worker at least (Deal)
 constexpr int kOverhead = 8;              // what beginning and ending a (request, head) costs, in pages
 constexpr int kJoin = 64, kJoinPart = 6;   // what a join by a warp costs, and each of its parts, in pages of a CTA
-constexpr int kWeightBits = 5, kScaleBits = 5;  // (Output, below) their sum and the slack of 5 make P < 2^15
+constexpr uint32_t kNoScale = 0x7180;     // (Output, below) f = 2^100: any scale outgrows it
 constexpr int kMaxParts = 2 * kWarps * kMaxCtas;
 
 struct Kv4AttnArgs {
@@ -162,13 +162,6 @@ __device__ __forceinline__ void unpack4(uint32_t w, uint32_t* e) {
     }
 }
 
-// both halves of a times half `h` of b
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b, int h) {
-    const __half2 s = *reinterpret_cast<__half2*>(&b);
-    const __half2 r = __hmul2_rn(*reinterpret_cast<__half2*>(&a), h ? __high2half2(s) : __low2half2(s));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 // Transpose of an 8 x 8 matrix of 16-bit values (two of a row to a lane)
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
     uint32_t d;
@@ -185,10 +178,10 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Two bf16 scales as fp16, times 2^(112 - o) with off = o << 7 of each: the exponent moved, both fields shifted into
-// place. Below the normal numbers of fp16 it is 0 (or, in the last step above, less than it should be), NaN stays NaN.
-__device__ __forceinline__ uint32_t scales_f16(uint32_t w, uint32_t off) {
-    return __viaddmin_s16x2_relu(w, off, 0x0FC00FC0u) << 3;
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
@@ -382,16 +375,13 @@ __device__ __noinline__ void join_parts(const Kv4AttnArgs& a, const Item& it, in
 //   accumulator of each group, 32 columns, in fp32; -sum s_k b_j for all keys and heads is one more tensor
 //   instruction, the scales as stored times b_j in three bf16 terms (24 bits), and starts the sum. (Codes with their
 //   bias are at most 15 where the values reach 7: the sums lose one bit to it.)
-//   Output. O^T[d, head] += V^T[d, key] P^T[key, head], P = rn(2^(x - M)) s_v[key, j] f_j, both factors and their product
-//   in fp16 (2^-11 for the first, 2^-11 for the product; s_v f_j is exact), V's codes exact (their bias would meet the sum
-//   of all weights, which grows with the length while the result does not). Products in packed halves take 18
-//   instructions a tile fewer than in fp32: 161 us for 512 requests of 1280 keys, else 167. f_j, a power of two that
-//   follows the largest scale of the group so far, is taken into a scale's exponent by integer arithmetic; M is the
-//   integral running maximum of the head less 5. They keep scales below 2^5 (the largest at 2^3 or more), weights below
-//   2^10 (the largest at 2^4 or more) and P below 2^15, and move only when a value has outgrown its limit, which one vote
-//   per two tiles detects. Below: weights cannot be nearer than 2^-25, P neither, scales under 2^-14 count as 0: 2^-26
-//   and 2^-29 of the group's largest scale a key, and 2^-14 of it in all. P goes from accumulator to operand layout by
-//   movmatrix.
+//   Output. O^T[d, head] += V^T[d, key] P^T[key, head], P = 2^(x - M) s_v[key, j] f_j, a product in fp32 that is rounded
+//   to fp16 once (2^-11; rounded before the product too, to form it in packed halves, 512 requests of 1280 keys take 153
+//   us instead of 157), V's codes exact (their bias would meet the sum of all weights, which grows with the length while
+//   the result does not). f_j, a power of two that follows the largest scale of the group so far, and M, the integral
+//   running maximum of the head, keep P below 2^15; both move only when a value has outgrown them (2^5 and 2^2 of slack),
+//   which one vote per two tiles detects. P cannot be nearer than 2^-25: 2^-29 of the group's largest scale a key. P goes
+//   from accumulator to operand layout by movmatrix.
 // Sums and statistics are fp32. M0, M1 etc. belong to the two head columns 2 t, 2 t + 1 of a lane.
 //
 // Work. Each CTA scans the lengths itself (no second launch, nothing on the host depends on them). With many (request,
@@ -554,10 +544,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
         if (k >= ahead) break;
         const int keys = s.item[warp][k & 1].keys;
         float O[NG][2][4], M0 = -INFINITY, M1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-        uint32_t f[NW];  // minus o << 7 of the groups: their scales count times 2^(112 - o)
+        uint32_t f[NW];  // of the groups, as bf16
 #pragma unroll
         for (int u = 0; u < NG; ++u) {
-            f[u / 2] = 0;
+            f[u / 2] = kNoScale * 0x10001u;
 #pragma unroll
             for (int i = 0; i < 4; ++i) O[u][0][i] = O[u][1][i] = 0.f;
         }
@@ -649,13 +639,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                     for (int e = 0; e < 4; ++e) yy[e] = ex2_approx(yy[e]);
                     l0 += yy[0] + yy[2];
                     l1 += yy[1] + yy[3];
-                    const uint32_t w0 = pack_f16x2(yy[0], yy[1]), w1 = pack_f16x2(yy[2], yy[3]);
 #pragma unroll
                     for (int u = 0; u < NW; ++u) {
-                        const uint32_t pa = scales_f16(tta[u], f[u]), pb = scales_f16(ttb[u], f[u]);
+                        const uint32_t pa = mul_bf16x2(tta[u], f[u]), pb = mul_bf16x2(ttb[u], f[u]);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const uint32_t b0 = transpose8(mul_f16x2(w0, pa, e)), b1 = transpose8(mul_f16x2(w1, pb, e));
+                            const float ga = e ? hi_bf16(pa) : lo_bf16(pa), gb = e ? hi_bf16(pb) : lo_bf16(pb);
+                            const uint32_t b0 = transpose8(pack_f16x2(yy[0] * ga, yy[1] * ga));
+                            const uint32_t b1 = transpose8(pack_f16x2(yy[2] * gb, yy[3] * gb));
                             uint32_t ea[4], eb[4];
                             unpack4<true>(va[2 * u + e], ea);
                             unpack4<true>(vb[2 * u + e], eb);
@@ -721,11 +712,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                             }
                         }
                     }
-                    constexpr uint32_t kFull = (15 + kScaleBits) << 7;  // of a scale's bits less o << 7
+                    constexpr uint32_t kFull = (2 * 127 + 10) << 7;  // of the bits of a scale and of f: s f reaches 2^10
                     uint32_t grown = 0;
 #pragma unroll
                     for (int u = 0; u < NW; ++u)
-                        grown |= __viaddmax_s16x2(max_bf16x2(max_bf16x2(ta[0][u], tb[0][u]), max_bf16x2(ta[1][u], tb[1][u])),
+                        grown |= __viaddmax_u16x2(max_bf16x2(max_bf16x2(ta[0][u], tb[0][u]), max_bf16x2(ta[1][u], tb[1][u])),
                                                   f[u], (kFull - 1) * 0x10001u) ^ (kFull - 1) * 0x10001u;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -736,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                     }
                     const float most = fmaxf(fmaxf(fmaxf(y[0][0], y[0][1]), fmaxf(y[0][2], y[0][3])),
                                              fmaxf(fmaxf(y[1][0], y[1][1]), fmaxf(y[1][2], y[1][3])));
-                    const bool over = most > 5.f + kWeightBits || grown;
+                    const bool over = most > 5.f || grown;
                     if (__any_sync(0xffffffffu, over)) {
                         // columns of heads beyond G are zeros throughout
                         float n0 = __fmul_rn(fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2])), hs0);
@@ -753,8 +744,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                             for (int u = 0; u < NW; ++u)
                                 top[u] = max_bf16x2(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
                         }
-                        n0 = softmax_max_update(M0, n0 - kWeightBits);
-                        n1 = softmax_max_update(M1, n1 - kWeightBits);
+                        n0 = softmax_max_update(M0, n0);
+                        n1 = softmax_max_update(M1, n1);
                         const float c0 = M0 == n0 ? 1.f : ex2_approx(M0 - n0), c1 = M1 == n1 ? 1.f : ex2_approx(M1 - n1);
                         M0 = n0;
                         M1 = n1;
@@ -762,14 +753,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                         l1 *= c1;
 #pragma unroll
                         for (int u = 0; u < NG; ++u) {
-                            const int was = u % 2 ? (int)f[u / 2] >> 16 : (int)(short)f[u / 2];
-                            const int t = u % 2 ? top[u / 2] >> 16 : top[u / 2] & 0xFFFFu;
+                            const uint32_t was = u % 2 ? f[u / 2] >> 16 : f[u / 2] & 0xFFFFu;
+                            const uint32_t t = u % 2 ? top[u / 2] >> 16 : top[u / 2] & 0xFFFFu;
                             float g = 1.f;
-                            if (t + was >= (int)kFull) {  // the new largest scale comes to [2^-2, 2^-1) of the most
-                                const int now = -(min((t >> 7) - 13 - kScaleBits, 215) << 7);
-                                f[u / 2] = u % 2 ? (f[u / 2] & 0xFFFFu) | (uint32_t)now << 16
-                                                 : (f[u / 2] & 0xFFFF0000u) | ((uint32_t)now & 0xFFFFu);
-                                g = __int_as_float(max(0, 127 + ((now - was) >> 7)) << 23);
+                            if (t + was >= kFull) {  // the new largest scale comes to [2^8, 2^9)
+                                const uint32_t now = (uint32_t)min(max(2 * 127 + 8 - (int)(t >> 7), 24), 254) << 7;
+                                f[u / 2] = u % 2 ? (f[u / 2] & 0xFFFFu) | now << 16 : (f[u / 2] & 0xFFFF0000u) | now;
+                                g = __int_as_float(max(0, 127 + (int)(now >> 7) - (int)(was >> 7)) << 23);
                             }
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
@@ -817,8 +807,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
         // rows of heads 2 t, 2 t + 1: columns 32 u + 4 g .. + 3
 #pragma unroll
         for (int u = 0; u < NG; ++u) {
-            const int o = -(u % 2 ? (int)f[u / 2] >> 16 : (int)(short)f[u / 2]);
-            const float g = __int_as_float((127 + 20 - 112 << 23) + (o << 16)), ge = g * 16.f;
+            // 2^20 and, for the even nibbles, 2^24, over f
+            const float g = __int_as_float(((2 * 127 + 20) << 23) - ((u % 2 ? f[u / 2] >> 16 : f[u / 2] & 0xFFFFu) << 16));
+            const float ge = g * 16.f;
             const float4 o0 = make_float4(O[u][0][0] * ge, O[u][0][2] * g, O[u][1][0] * ge, O[u][1][2] * g);
             const float4 o1 = make_float4(O[u][0][1] * ge, O[u][0][3] * g, O[u][1][1] * ge, O[u][1][3] * g);
             const int col = 32 * u + 4 * gid;
