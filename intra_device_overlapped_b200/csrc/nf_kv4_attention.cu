@@ -84,6 +84,7 @@ struct Smem {
     int64_t pos[kWarps];  // the place where the warp's next stretch begins
     Deal deal;
     int last[2];
+    int4 rest[kWarps];  // what exact_rest goes on from: k, ahead, more, pending
 };
 
 // Pages that request r reads: its keys, cut to what its row of the page table holds; *at: where the row begins.
@@ -299,6 +300,147 @@ __device__ __forceinline__ void store_out(const Kv4AttnArgs& a, const Item& it, 
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
+// A number 0..15 less 8 (no conversion instruction)
+__device__ __forceinline__ float code_of(uint32_t nibble) {
+    return __uint_as_float((nibble & 15u) | 0x4B000000u) - 8388616.f;
+}
+
+// The sums of a stretch (its pages `offset` and `offset` + 1 of every `step`) in fp32 throughout, to the team's memory,
+// the output or the workspace. A key at a time, read from the pool again: lane (g, t) takes columns 4 g .. 4 g + 3 of
+// each group for heads 2 t and 2 t + 1, in scores and output alike.
+template <int D>
+__device__ __forceinline__ void exact_sums(const Kv4AttnArgs& a, Smem<D>& sm, const Item& it, int offset, int step) {
+    constexpr int NG = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, h0 = 2 * (lane & 3);
+    uint2 q[2][NG];
+    float m[2], hs[2], M[2], l[2], sum[2][NG][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint16_t* const row = a.q + it.r * a.q_stride + (int64_t)(it.h * a.G + min(h0 + i, a.G - 1)) * D + 4 * gid;
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            q[i][j] = *reinterpret_cast<const uint2*>(row + 32 * j);
+            top = max(top, max(max(q[i][j].x & 0x7FFFu, q[i][j].x >> 16 & 0x7FFFu),
+                               max(q[i][j].y & 0x7FFFu, q[i][j].y >> 16 & 0x7FFFu)));
+            sum[i][j][0] = sum[i][j][1] = sum[i][j][2] = sum[i][j][3] = 0.f;
+        }
+#pragma unroll
+        for (int of = 4; of < 32; of <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, of));
+        // q over 2^e, its row's largest or nearly so, as at the kernel
+        const int ex = min(max((int)(top >> 7), 1), 253);
+        m[i] = __int_as_float((254 - ex) << 23);
+        hs[i] = fminf(fmaxf(a.scale_log2 * __int_as_float(ex << 23), 0x1p-140f), 0x1p127f);
+        M[i] = -INFINITY;
+        l[i] = 0.f;
+    }
+#pragma unroll 1
+    for (int p = offset; p < it.pages; p += p & 1 ? step - 1 : 1) {  // (offset is even)
+        const int id = __ldg(a.indices + it.first + p);
+        if ((unsigned)id >= (unsigned)a.num_pages) continue;
+        const uint8_t* const kt = a.pool + ((int64_t)id * a.nkv + it.h) * (18 * D);
+        const uint8_t* const vt = kt + 9 * D;
+        const int n = min(it.keys - p * kKv4Slots, kKv4Slots);
+#pragma unroll 1
+        for (int s = 0; s < n; ++s) {
+            uint32_t kw[NG], ks[NG / 2], vw[NG], vs[NG / 2];
+            load_words<NG>(kt + s * (D / 2) + (gid >> 1) * (D / 8), kw);
+            load_scales<NG>(kt + 8 * D + s * (2 * NG), ks);
+            load_words<NG>(vt + (s >> 3) * 4 * D + ((s & 7) >> 1) * D + gid * (D / 8), vw);
+            load_scales<NG>(vt + 8 * D + s * (2 * NG), vs);
+            float x[2] = {0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                const uint32_t v = kw[j] >> 8 * (gid & 1);
+                const float c0 = code_of(v), c1 = code_of(v >> 16), c2 = code_of(v >> 4), c3 = code_of(v >> 20);
+                const float g = j % 2 ? hi_bf16(ks[j / 2]) : lo_bf16(ks[j / 2]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float dot = lo_bf16(q[i][j].x) * m[i] * c0;
+                    dot = fmaf(hi_bf16(q[i][j].x) * m[i], c1, dot);
+                    dot = fmaf(lo_bf16(q[i][j].y) * m[i], c2, dot);
+                    dot = fmaf(hi_bf16(q[i][j].y) * m[i], c3, dot);
+                    x[i] = fmaf(g, dot, x[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int of = 4; of < 32; of <<= 1) x[i] += __shfl_xor_sync(0xffffffffu, x[i], of);
+                x[i] = __fmul_rn(x[i], hs[i]);
+                const float now = softmax_max_update(M[i], x[i]);
+                if (now != M[i]) {
+                    const float c = ex2_approx(M[i] - now);
+                    M[i] = now;
+                    l[i] *= c;
+#pragma unroll
+                    for (int j = 0; j < NG; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sum[i][j][e] *= c;
+                }
+                x[i] = x[i] == -INFINITY ? 0.f : ex2_approx(x[i] - M[i]);
+                l[i] += x[i];
+            }
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                const uint32_t v = vw[j] >> 16 * (s & 1);
+                const float g = j % 2 ? hi_bf16(vs[j / 2]) : lo_bf16(vs[j / 2]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum[i][j][e] = fmaf(x[i] * g, code_of(v >> 4 * e), sum[i][j][e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int h = h0 + i;
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            const int col = 32 * j + 4 * gid;
+            const float4 o = make_float4(sum[i][j][0], sum[i][j][1], sum[i][j][2], sum[i][j][3]);
+            if (sm.deal.chunk)
+                *reinterpret_cast<float4*>(sm.merge(warp, h) + col) = o;
+            else if (h < a.G && it.parts == 1)
+                store_out(a, it, D, h, col, o, l[i]);
+            else if (h < a.G)
+                __stcg(reinterpret_cast<float4*>(a.part_o + ((int64_t)part_slot(it, it.c) * a.G + h) * D + col), o);
+        }
+        if (gid == 0 && sm.deal.chunk)
+            sm.ml[warp][h] = make_float2(M[i], l[i]);
+        else if (gid == 0 && it.parts > 1)
+            __stcg(a.part_ml + (int64_t)part_slot(it, it.c) * kMaxGroup + h, make_float2(M[i], l[i]));
+    }
+}
+
+// The rest of the warp's share by exact_sums, from a stretch on whose fp16 weights may have lost something (Output, at the
+// kernel). Returns the parts to be reported. The warp does not come back to the tensor instructions: kept alive across
+// this call, the state of their loop cost registers, and 512 requests of 1280 keys 6 % of their time.
+template <int D>
+__device__ __noinline__ int exact_rest(const Kv4AttnArgs& a, Smem<D>& s) {
+    const int warp = threadIdx.x >> 5;
+    int k = s.rest[warp].x, ahead = s.rest[warp].y, pending = s.rest[warp].w;
+    bool more = s.rest[warp].z;
+    const int offset = s.deal.chunk ? 2 * warp : 0, step = s.deal.chunk ? 2 * kWarps : 2;
+#pragma unroll 1
+    for (;; ++k) {
+        Item& it = s.item[warp][k & 1];
+        if (k == ahead) {
+            do {
+                if (!more) return pending;
+                more = find_item<D>(a, s, &it);
+            } while (it.r < 0);
+            ++ahead;
+        }
+        exact_sums<D>(a, s, it, offset, step);
+        if (it.parts > 1) {
+            if ((threadIdx.x & 31) == 0) s.pending[warp][pending] = it;
+            ++pending;
+        }
+        __syncwarp();
+    }
+}
+
 // Parts of a (request, head), joined in order into the output by one warp: heads h0 .. h0 + H - 1, 4 columns of a head
 // to a lane. The weights of 32 / H parts are formed by a lane each; rows of 4 parts are loaded at a time, the first before
 // the maximum is known. One body for any number of parts (the last is loaded again, with weight 0, for those that are
@@ -380,8 +522,13 @@ __device__ __noinline__ void join_parts(const Kv4AttnArgs& a, const Item& it, in
 //   us instead of 157), V's codes exact (their bias would meet the sum of all weights, which grows with the length while
 //   the result does not). f_j, a power of two that follows the largest scale of the group so far, and M, the integral
 //   running maximum of the head, keep P below 2^15; both move only when a value has outgrown them (2^5 and 2^2 of slack),
-//   which one vote per two tiles detects. P cannot be nearer than 2^-25: 2^-29 of the group's largest scale a key. P goes
-//   from accumulator to operand layout by movmatrix.
+//   which one vote per two tiles detects. P goes from accumulator to operand layout by movmatrix.
+//   P is 2^-25 off at most where it is below fp16's normal numbers, and counts for nothing below that: with scales far
+//   from one another, or zeros, at the keys that weigh most, this may be all that a head gets from a group. So a stretch
+//   of n keys is taken for good where, for each head and group with any scale, the largest of the 32 sums is n 2^-10 in P's
+//   units or more (2^6 from 2^16 keys on): what is lost, at most n 2^-25 times 7, is then 2^-12 of it (n 2^-28). In a head
+//   whose heaviest key has the largest scale P reaches 2^7 and its sums 7 times that. Otherwise the warp takes this stretch,
+//   and the rest of its share, in fp32 (exact_rest): 15 times the time. The comparison costs 0.6 us of 165.
 // Sums and statistics are fp32. M0, M1 etc. belong to the two head columns 2 t, 2 t + 1 of a lane.
 //
 // Work. Each CTA scans the lengths itself (no second launch, nothing on the host depends on them). With many (request,
@@ -796,19 +943,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
             l0 += __shfl_xor_sync(0xffffffffu, l0, o);
             l1 += __shfl_xor_sync(0xffffffffu, l1, o);
         }
-        const Item it = s.item[warp][k & 1];
-        if (team()) {  // (one stretch: the sums have their memory for themselves)
-            if (gid == 0) {
-                s.ml[warp][2 * tig] = make_float2(M0, l0);
-                s.ml[warp][2 * tig + 1] = make_float2(M1, l1);
+        bool lost = false;
+        const int seen = s.item[warp][k & 1].keys;
+        if (seen > offset() * kKv4Slots) {
+            // (Output, above) the least that the largest sum of a group has to be, in the accumulators' units
+            const float least = 0x1p-20f * fminf(0x1p-10f * (team() ? seen / kWarps + 2 * kKv4Slots : seen), 64.f);
+#pragma unroll
+            for (int u = 0; u < NG; ++u) {
+                const bool any = (u % 2 ? f[u / 2] >> 16 : f[u / 2] & 0xFFFFu) != kNoScale;  // else all zeros
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float most = fmaxf(fmaxf(fabsf(O[u][0][e]), fabsf(O[u][1][e])) * 16.f,
+                                             fmaxf(fabsf(O[u][0][2 + e]), fabsf(O[u][1][2 + e])));
+                    const uint32_t enough = __ballot_sync(0xffffffffu, !(most < least));
+                    lost |= any && 2 * tig + e < a.G && !(enough & 0x11111111u << tig);
+                }
             }
+            lost = __any_sync(0xffffffffu, lost);
         }
+        if (lost) {
+            if (lane == 0) s.rest[warp] = make_int4(k, ahead, more, pending);
+            pending = -1;
+            break;
+        }
+        const Item it = s.item[warp][k & 1];
         const int64_t part = part_slot(it, it.c);
+        if (gid == 0 && team()) {  // (one stretch: the sums have their memory for themselves)
+            s.ml[warp][2 * tig] = make_float2(M0, l0);
+            s.ml[warp][2 * tig + 1] = make_float2(M1, l1);
+        }
         // rows of heads 2 t, 2 t + 1: columns 32 u + 4 g .. + 3
 #pragma unroll
         for (int u = 0; u < NG; ++u) {
             // 2^20 and, for the even nibbles, 2^24, over f
-            const float g = __int_as_float(((2 * 127 + 20) << 23) - ((u % 2 ? f[u / 2] >> 16 : f[u / 2] & 0xFFFFu) << 16));
+            const float g = __uint_as_float(((2 * 127 + 20) << 23) - ((u % 2 ? f[u / 2] >> 16 : f[u / 2] & 0xFFFFu) << 16));
             const float ge = g * 16.f;
             const float4 o0 = make_float4(O[u][0][0] * ge, O[u][0][2] * g, O[u][1][0] * ge, O[u][1][2] * g);
             const float4 o1 = make_float4(O[u][0][1] * ge, O[u][0][3] * g, O[u][1][1] * ge, O[u][1][3] * g);
@@ -825,33 +993,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                 if (2 * tig + 1 < a.G) __stcg(reinterpret_cast<float4*>(po + D), o1);
             }
         }
-        if (team()) {
-            __syncthreads();
-            const int col = tid % (D / 4) * 4, h = tid / (D / 4);  // thread -> 4 columns of one head
-            if (h < a.G) {
-                float M = -INFINITY, L = 0.f;
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s.ml[w][h].x);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float2 ml = s.ml[w][h];
-                    const float c = part_factor(ml.x, M);
-                    const float4 v = *reinterpret_cast<const float4*>(s.merge(w, h) + col);
-                    L += c * ml.y;
-                    o.x += c * v.x;
-                    o.y += c * v.y;
-                    o.z += c * v.z;
-                    o.w += c * v.w;
-                }
-                if (it.parts == 1) {
-                    store_out(a, it, D, h, col, o, L);
-                } else {
-                    __stcg(reinterpret_cast<float4*>(a.part_o + (part * a.G + h) * D + col), o);
-                    if (col == 0) __stcg(a.part_ml + part * kMaxGroup + h, make_float2(M, L));
-                }
-            }
-        }
         if (it.parts > 1) {
             if (!team() && gid == 0) {
                 __stcg(a.part_ml + part * kMaxGroup + 2 * tig, make_float2(M0, l0));
@@ -859,6 +1000,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
             }
             if (lane == 0) s.pending[warp][pending] = it;
             ++pending;
+        }
+    }
+    if (pending < 0) {
+        cp_async_wait<0>();  // (nothing more is taken from the ring)
+        __syncwarp();
+        pending = exact_rest<D>(a, s);
+    }
+    if (team() && blockIdx.x < s.deal.total) {  // its one stretch
+        __syncthreads();
+        const Item& it = s.item[warp][0];
+        const int col = tid % (D / 4) * 4, h = tid / (D / 4);  // thread -> 4 columns of one head
+        if (h < a.G) {
+            float M = -INFINITY, L = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s.ml[w][h].x);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 ml = s.ml[w][h];
+                const float c = part_factor(ml.x, M);
+                const float4 v = *reinterpret_cast<const float4*>(s.merge(w, h) + col);
+                L += c * ml.y;
+                o.x += c * v.x;
+                o.y += c * v.y;
+                o.z += c * v.z;
+                o.w += c * v.w;
+            }
+            if (it.parts == 1) {
+                store_out(a, it, D, h, col, o, L);
+            } else {
+                const int64_t part = part_slot(it, it.c);
+                __stcg(reinterpret_cast<float4*>(a.part_o + (part * a.G + h) * D + col), o);
+                if (col == 0) __stcg(a.part_ml + part * kMaxGroup + h, make_float2(M, L));
+            }
         }
     }
     if (pending) {  // (all warps of a team have the same)

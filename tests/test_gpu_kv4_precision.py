@@ -106,3 +106,110 @@ def test_a_weight_rounds_once(nf):
             bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * x_err + 2.0 ** -21) * mass
             err = np.abs(gh[r, 8 * h:8 * h + 8] - want)
             assert (err <= bound).all(), (r, h, float((err - bound).max()))
+
+
+def _set_key(c, r, at, which, head, scales=None, codes=None):
+    """Key `at` of request r: its scales (one per group, None: as they are) and codes [d] in -7..7."""
+    page, slot = c.indices[c.indptr[r] + at // 16], at % 16
+    tile = c.host.raw[page, head, which]
+    if scales is not None:
+        n = 8 * c.d + slot * (c.d // 32) * 2
+        for j, s in enumerate(scales):
+            if s is not None:
+                tile[n + 2 * j:n + 2 * j + 2] = ref.to_bits(np.array([s])).view(np.uint8)
+    if codes is not None:
+        for hf in (0, 1):
+            cols = np.nonzero(c.host.half[which, slot] == hf)[0]
+            b = c.host.byte[which, slot, cols]
+            tile[b] = (tile[b] & (0xF0 if hf == 0 else 0x0F)) | ((codes[cols] + 8) << (4 * hf)).astype(np.uint8)
+
+
+def _biased(c, q, keys, log2_weight, head):
+    """The keys' scores at `head` lower by `log2_weight` than they would be at 0: column 0 of q is 4 for every head."""
+    d = c.d
+    codes = np.zeros(d, dtype=np.int64)
+    codes[0] = -7
+    for r, at in keys:
+        scale = log2_weight * math.log(2) * math.sqrt(d) / (4 * 7)
+        _set_key(c, r, at, 0, head, scales=[scale] + [0.0] * (d // 32 - 1), codes=codes)
+
+
+OUTLIERS = [  # log2 of the weight that a key loses, log2 of its values' magnitude
+    (100, 40), (60, 57), (30, 30), (20, 18), (40, 25), (12, 10), (40, 17), (25, 24), (0, 17), (0, -40)]
+
+
+@pytest.mark.parametrize("lens,nq,nkv,d", [([2, 16, 40], 8, 2, 128), ([700, 33], 12, 2, 64), ([3000], 8, 1, 128),
+                                           ([90, 100, 17, 64] * 12, 16, 4, 128)], ids=str)
+@pytest.mark.parametrize("below,above", OUTLIERS)
+def test_keys_of_little_weight_and_large_values(nf, lens, nq, nkv, d, below, above):
+    """Keys with values 2^above times the others' and weights 2^-below of theirs, in some groups of columns or all: they
+    count for what they are, and so do the others."""
+    rng = np.random.default_rng(below * 64 + abs(above) + len(lens))
+    c = Cache(lens, nkv, d, seed=below + len(lens), spread=0.5)
+    q = rng.standard_normal((len(lens), nq, d))
+    q[..., 0] = 4.0
+    ng = d // 32
+    for r, n in enumerate(lens):
+        for head in range(nkv):
+            keys = sorted({int(x) for x in rng.integers(0, n, max(1, n // 300))} - ({0} if n == 2 else set()))
+            _biased(c, q, [(r, k) for k in keys], below, head)
+            groups = range(ng) if (r + head) % 2 else [head % ng, ng - 1]
+            for k in keys:
+                _set_key(c, r, k, 1, head, [0.15 * 2.0 ** above if j in groups else None for j in range(ng)])
+    c.upload()
+    q = _dev(q.astype(np.float32), torch.bfloat16)
+    for sm in (0, 3):
+        _check(c, q, _run(nf, c, q, sm=sm), rows=range(min(len(lens), 6)))
+
+
+@pytest.mark.parametrize("lens,nq,nkv,d", [([2], 1, 1, 64), ([40, 300], 8, 2, 128), ([2500] * 3, 16, 2, 128)], ids=str)
+@pytest.mark.parametrize("weight", [20, 35, 60])
+def test_the_key_that_weighs_most_has_no_values(nf, lens, nq, nkv, d, weight):
+    """One key takes nearly all the weight and holds zeros in some groups: the others' values are what is left there. A
+    group without values in any key is exactly 0."""
+    rng = np.random.default_rng(weight)
+    c = Cache(lens, nkv, d, seed=weight, spread=0.25)
+    q = rng.standard_normal((len(lens), nq, d)) * 0.5
+    q[..., 0] = 4.0
+    ng = d // 32
+    for r, n in enumerate(lens):
+        for head in range(nkv):
+            k = int(rng.integers(0, n))
+            _biased(c, q, [(r, at) for at in range(n) if at != k], weight, head)
+            _set_key(c, r, k, 1, head, [0.0 if j % 2 == 0 else None for j in range(ng)])
+            if ng == 4:
+                for at in range(n):
+                    _set_key(c, r, at, 1, head, [None, None, None, 0.0])
+    c.upload()
+    q = _dev(q.astype(np.float32), torch.bfloat16)
+    out = _run(nf, c, q)
+    _check(c, q, out)
+    if ng == 4:
+        assert (out[..., 96:] == 0).all() and (out[..., :32] != 0).any()
+
+
+def test_outliers_beside_missing_pages_and_nan(nf):
+    """A key of large values and no weight in a request with a page outside the pool, and one with a NaN scale."""
+    c = Cache([70, 70], 1, 128, seed=21)
+    q = np.random.default_rng(4).standard_normal((2, 8, 128))
+    q[..., 0] = 4.0
+    for r in (0, 1):
+        _biased(c, q, [(r, 5)], 80, 0)
+        _set_key(c, r, 5, 1, 0, [2.0 ** 35] * 4)
+    _set_key(c, 1, 9, 1, 0, [None, math.nan, None, None])
+    c.upload()
+    clean = c.indices.copy()
+    c.indices[c.indptr[0] + 2] = c.pages + 7
+    c.dev[2] = torch.from_numpy(c.indices.astype(np.int32)).cuda()
+    q = _dev(q.astype(np.float32), torch.bfloat16)
+    out, ws, status = torch.full_like(q, float("nan")), _workspace(nf, 8, 1, 128), _status()
+    _attend(nf, c, q, out, ws, status)
+    torch.cuda.synchronize()
+    assert int(status) == nf.NF_ERR_DEVICE_BOUNDS
+    nan = torch.isnan(out).cpu().numpy()
+    assert nan[1, :, 32:64].all() and nan.sum() == 8 * 32
+    c.indices = clean
+    K, V = (x[0, np.r_[0:32, 48:70]] for x in c.keys(0))
+    keep = lambda r: (K[None], V[None])  # noqa: E731
+    c.keys = keep
+    _check(c, q, out, rows=[0])
