@@ -612,7 +612,8 @@ int64_t nf_kv4_workspace_bytes(int32_t n_q_heads, int32_t n_kv_heads, int32_t he
  * sums in fp32; the weights that multiply V, scaled by V's scales, are rounded to fp16 once (2^-11); those too
  * small for fp16 come, for all keys together, to at most 2^-12 of the largest sum of weights times |V| among the same 32
  * columns (2^-28 of it a key where one warp reads more than 2^16 keys). Values whose scales differ so far that more
- * would be lost are summed in fp32, at a fraction of the speed. The order of
+ * would be lost are summed in fp32, at a fraction of the speed, and so are the scores of a row of q that has 32 columns
+ * (from a multiple of 32 on) whose largest is below 2^-11 of the row's. The order of
  * the sums follows the batch's lengths and sm_count, not the run: equal calls give equal bits.
  * num_pages * n_kv_heads is at most 2^31 - 1, else NF_ERR_INVALID_ARGUMENT. */
 nf_status nf_op_kv4_decode_attention(const void* q, int64_t q_stride, void* out, int64_t out_stride, const void* pool,

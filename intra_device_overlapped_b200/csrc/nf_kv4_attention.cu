@@ -307,7 +307,8 @@ __device__ __forceinline__ float code_of(uint32_t nibble) {
 
 // The sums of a stretch (its pages `offset` and `offset` + 1 of every `step`) in fp32 throughout, to the team's memory,
 // the output or the workspace. A key at a time, read from the pool again: lane (g, t) takes columns 4 g .. 4 g + 3 of
-// each group for heads 2 t and 2 t + 1, in scores and output alike.
+// each group for heads 2 t and 2 t + 1, in scores and output alike. About 300 instructions a key, where the tensor
+// instructions' loop takes 19.
 template <int D>
 __device__ __forceinline__ void exact_sums(const Kv4AttnArgs& a, Smem<D>& sm, const Item& it, int offset, int step) {
     constexpr int NG = D / 32;
@@ -413,8 +414,8 @@ __device__ __forceinline__ void exact_sums(const Kv4AttnArgs& a, Smem<D>& sm, co
     }
 }
 
-// The rest of the warp's share by exact_sums, from a stretch on whose fp16 weights may have lost something (Output, at the
-// kernel). Returns the parts to be reported. The warp does not come back to the tensor instructions: kept alive across
+// The rest of the warp's share by exact_sums, from a stretch on whose fp16 weights or q may have lost something (Scores and
+// Output, at the kernel). Returns the parts to be reported. The warp does not come back to the tensor instructions: kept alive across
 // this call, the state of their loop cost registers, and 512 requests of 1280 keys 6 % of their time.
 template <int D>
 __device__ __noinline__ int exact_rest(const Kv4AttnArgs& a, Smem<D>& s) {
@@ -516,7 +517,9 @@ __device__ __noinline__ void join_parts(const Kv4AttnArgs& a, const Item& it, in
 //   even nibbles times 16 for their codes' 2^-24), b_j = sum of bias times q. The scale is applied to the 16 x 8
 //   accumulator of each group, 32 columns, in fp32; -sum s_k b_j for all keys and heads is one more tensor
 //   instruction, the scales as stored times b_j in three bf16 terms (24 bits), and starts the sum. (Codes with their
-//   bias are at most 15 where the values reach 7: the sums lose one bit to it.)
+//   bias are at most 15 where the values reach 7: the sums lose one bit to it.) A column of q is off by 2^-35 of its row's
+//   largest at most. Where that is more than 2^-24 of the largest in its group, whose K may be as much larger, the stretch
+//   goes to exact_rest.
 //   Output. O^T[d, head] += V^T[d, key] P^T[key, head], P = 2^(x - M) s_v[key, j] f_j, a product in fp32 that is rounded
 //   to fp16 once (2^-11; rounded before the product too, to form it in packed halves, 512 requests of 1280 keys take 153
 //   us instead of 157), V's codes exact (their bias would meet the sum of all weights, which grows with the length while
@@ -698,6 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
 #pragma unroll
             for (int i = 0; i < 4; ++i) O[u][0][i] = O[u][1][i] = 0.f;
         }
+        bool lost = false;
         if (keys > offset() * kKv4Slots) {
             if (flying == kStages)  // the first pair, and q with it
                 cp_async_wait<kStages - 1>();
@@ -712,20 +716,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
 #pragma unroll
                 for (int j = 0; j < NG; ++j) sum[j] = 0.f;
                 uint4 raw[NG];
-                uint32_t top = 0;
+                uint32_t tops[NW] = {};  // the largest of each group
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
                     raw[j] = gid < a.G ? *reinterpret_cast<const uint4*>(&s.q[warp][k & 1][gid * D + 32 * j + 8 * tig])
                                        : make_uint4(0, 0, 0, 0);
-                    const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, w[i] >> 16 & 0x7FFFu));
+                    const uint32_t both = __vmaxu2(__vmaxu2(raw[j].x & 0x7FFF7FFFu, raw[j].y & 0x7FFF7FFFu),
+                                                   __vmaxu2(raw[j].z & 0x7FFF7FFFu, raw[j].w & 0x7FFF7FFFu));
+                    tops[j / 2] |= max(both & 0xFFFFu, both >> 16) << 16 * (j % 2);
                 }
                 __syncwarp();  // all have read their q
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                uint32_t top = 0;
+#pragma unroll
+                for (int u = 0; u < NW; ++u) {
+                    tops[u] = __vmaxu2(tops[u], __shfl_xor_sync(0xffffffffu, tops[u], 1));
+                    tops[u] = __vmaxu2(tops[u], __shfl_xor_sync(0xffffffffu, tops[u], 2));
+                    top = max(top, max(tops[u] & 0xFFFFu, tops[u] >> 16));
+                }
                 // exponent field; rows of zeros or subnormals count as 1, infinities and NaN as 254
                 const int ex = min(max((int)(top >> 7), 1), 254);
+#pragma unroll
+                for (int u = 0; u < NW; ++u) {
+                    // (Scores, above) a group of small q, 2^-11 of the row's or less
+                    const int lo = tops[u] & 0xFFFFu, hi = tops[u] >> 16;
+                    lost |= (lo && (lo >> 7) + 11 < ex) || (hi && (hi >> 7) + 11 < ex);
+                }
+                lost = __any_sync(0xffffffffu, lost);
                 // 2^(10 - (ex - 127)) in two steps, either a normal number
                 const int up = 10 + 127 - ex, up0 = up / 2, up1 = up - up0;
                 const float m0 = __int_as_float((127 + up0) << 23), m1 = __int_as_float((127 + up1) << 23);
@@ -765,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                 s.bias[warp][lane] = make_uint4(term(sum[0], sum[1]), NW == 2 ? term(sum[NG - 2], sum[NG - 1]) : 0,
                                                 __float_as_uint(hs0), __float_as_uint(hs1));
             }
-            for (int left = keys - offset() * kKv4Slots; left > 0; left -= step * kKv4Slots) {  // keys from the pair on
+            for (int left = lost ? 0 : keys - offset() * kKv4Slots; left > 0; left -= step * kKv4Slots) {  // keys from the pair on
                 if (flying < kStages) fill(k);  // (a new stretch to begin)
                 if (flying == kStages)
                     cp_async_wait<kStages - 1>();
@@ -943,9 +959,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
             l0 += __shfl_xor_sync(0xffffffffu, l0, o);
             l1 += __shfl_xor_sync(0xffffffffu, l1, o);
         }
-        bool lost = false;
         const int seen = s.item[warp][k & 1].keys;
-        if (seen > offset() * kKv4Slots) {
+        if (!lost && seen > offset() * kKv4Slots) {
             // (Output, above) the least that the largest sum of a group has to be, in the accumulators' units
             const float least = 0x1p-20f * fminf(0x1p-10f * (team() ? seen / kWarps + 2 * kKv4Slots : seen), 64.f);
 #pragma unroll

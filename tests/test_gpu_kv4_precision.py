@@ -213,3 +213,27 @@ def test_outliers_beside_missing_pages_and_nan(nf):
     keep = lambda r: (K[None], V[None])  # noqa: E731
     c.keys = keep
     _check(c, q, out, rows=[0])
+
+
+@pytest.mark.parametrize("lens,nq,nkv,d", [([1, 5, 64], 8, 2, 128), ([900], 3, 1, 64), ([200] * 30, 16, 8, 128)], ids=str)
+@pytest.mark.parametrize("down", [9, 11, 12, 14, 20, 30, 45, 70])
+def test_columns_of_small_q_meet_large_k(nf, lens, nq, nkv, d, down):
+    """q's columns of one group are 2^-down of the others, K's 2^down of theirs: they make the scores alike. One row of
+    q has zeros there, one nothing but them."""
+    rng = np.random.default_rng(down + len(lens))
+    c = Cache(lens, nkv, d, seed=down)
+    at = d // 32 - 1
+    bits = _scales(c, 0).copy()
+    f = ref.from_bits(bits)
+    half = down // 2
+    f = np.where(np.isnan(f), f, f * 2.0 ** np.where(np.arange(d // 32) == at, half, half - down))
+    _put(c, 0, ref.to_bits(f))
+    c.upload()
+    q = rng.standard_normal((len(lens), nq, d)) * 2.0 ** (down - half)
+    q[..., 32 * at:] *= 2.0 ** -down
+    q[0, 0, 32 * at:] = 0.0
+    q[0, -1, :32 * at] = 0.0
+    q = _dev(q.astype(np.float32), torch.bfloat16)
+    out = _run(nf, c, q)
+    _check(c, q, out, rows=range(min(len(lens), 5)))
+    _run(nf, c, q, sm=2)
