@@ -12,6 +12,7 @@ namespace nf {
 namespace {
 
 constexpr int kMapThreads = 1024;
+constexpr size_t kMapScratch = sizeof(int64_t) * kMapThreads / 32;  // static shared memory
 
 struct PageMapArgs {
     const int *ctx_len, *new_len;
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const PageMapArgs
     int* page_off = sm;                    // [R + 1]
     int* tok_off = page_off + a.R + 1;     // [R + 1]
     int* take_off = tok_off + a.R + 1;     // [R]: first new page's place in the order; -1: refused
-    __shared__ int64_t scratch[32];
+    __shared__ int64_t scratch[kMapScratch / sizeof(int64_t)];
     const int tid = threadIdx.x;
     const bool first = blockIdx.x == 0;
     const int per = (a.R + kMapThreads - 1) / kMapThreads;
@@ -243,8 +244,9 @@ extern "C" nf_status nf_op_page_map(const int32_t* ctx_len, const int32_t* new_l
     grid = grid < 1 ? 1 : grid > sms ? sms : grid;
     const size_t smem = sizeof(int) * ((size_t)3 * num_requests + 2);
     static_assert(sizeof(int) * (3 * NF_KV4_MAX_REQUESTS + 2) <= 224 * 1024, "offsets fit shared memory");
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(nf::page_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)smem) != cudaSuccess)
+    // (48 KB without opting in, those of `scratch` among them)
+    if (smem + nf::kMapScratch > 48 * 1024 &&
+        cudaFuncSetAttribute(nf::page_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return NF_ERR_CUDA;
     const nf::PageMapArgs a{ctx_len, new_len, num_requests, block_table, table_stride, free_pages, free_cap, free_count,
                             num_pages, kv_len, page_indptr, page_indices, page_cap, slots, positions, token_cap,
