@@ -243,10 +243,12 @@ extern "C" nf_status nf_op_page_map(const int32_t* ctx_len, const int32_t* new_l
     int64_t grid = (entries + nf::kMapThreads - 1) / nf::kMapThreads;
     grid = grid < 1 ? 1 : grid > sms ? sms : grid;
     const size_t smem = sizeof(int) * ((size_t)3 * num_requests + 2);
-    static_assert(sizeof(int) * (3 * NF_KV4_MAX_REQUESTS + 2) <= 224 * 1024, "offsets fit shared memory");
-    // (48 KB without opting in, those of `scratch` among them)
+    constexpr int kMost = sizeof(int) * (3 * NF_KV4_MAX_REQUESTS + 2);
+    static_assert(kMost + nf::kMapScratch <= 227 * 1024, "offsets fit shared memory");
+    // 48 KB without opting in, those of `scratch` among them. The limit is the kernel's, whichever thread sets it and for
+    // captured calls too: always the largest, so that no call lowers what another one needs.
     if (smem + nf::kMapScratch > 48 * 1024 &&
-        cudaFuncSetAttribute(nf::page_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        cudaFuncSetAttribute(nf::page_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess)
         return NF_ERR_CUDA;
     const nf::PageMapArgs a{ctx_len, new_len, num_requests, block_table, table_stride, free_pages, free_cap, free_count,
                             num_pages, kv_len, page_indptr, page_indices, page_cap, slots, positions, token_cap,
