@@ -441,9 +441,10 @@ def _own(s):
             s["v"].data_ptr(), nkv * d, DTYPES[c.get("out", "bf16")][1], status, stream))
     else:
         size = nf.nf_kv4_workspace_bytes(c["nq"], nkv, d)
-        held = _workspaces.get(size)
-        if held is None:  # zeroed once, kept by the program for all its calls
-            held = _workspaces[size] = torch.zeros(size, dtype=torch.uint8, device="cuda")
+        place = (size, torch.cuda.current_device(), stream)
+        held = _workspaces.get(place)
+        if held is None:  # zeroed once on the stream that uses it, kept by the program for all its calls there
+            held = _workspaces[place] = torch.zeros(size, dtype=torch.uint8, device="cuda")
         nf.check(nf.nf_op_kv4_decode_attention(
             s["q"].data_ptr(), c["nq"] * d, s["out"].data_ptr(), c["nq"] * d, s["pool"].data_ptr(), s["pages"],
             s["kv_len"].data_ptr(), s["indptr"].data_ptr(), s["indices"].data_ptr(), c["requests"], c["nq"], nkv, d,
