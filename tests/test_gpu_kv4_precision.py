@@ -237,3 +237,44 @@ def test_columns_of_small_q_meet_large_k(nf, lens, nq, nkv, d, down):
     out = _run(nf, c, q)
     _check(c, q, out, rows=range(min(len(lens), 5)))
     _run(nf, c, q, sm=2)
+
+
+@pytest.mark.parametrize("lens,nq,nkv", [([40, 900, 7], 8, 2), ([60] * 40, 24, 8)], ids=str)
+def test_outliers_in_place_and_called_again(nf, lens, nq, nkv):
+    """The output over q, call after call with one workspace, gives the same bits; the workspace's counters are at 0 again."""
+    d = 128
+    c = Cache(lens, nkv, d, seed=31)
+    q = np.random.default_rng(6).standard_normal((len(lens), nq, d))
+    q[..., 0] = 4.0
+    for r in range(0, len(lens), 2):
+        for head in range(nkv):
+            _biased(c, q, [(r, 3)], 70, head)
+            _set_key(c, r, 3, 1, head, [2.0 ** 30] * 4)
+    c.upload()
+    q = _dev(q.astype(np.float32), torch.bfloat16)
+    want = _run(nf, c, q)
+    _check(c, q, want, rows=range(min(len(lens), 6)))
+    ws, status = _workspace(nf, nq, nkv, d), _status()
+    for _ in range(3):
+        both = q.clone()
+        _attend(nf, c, both, both, ws, status)
+        torch.cuda.synchronize()
+        assert torch.equal(both, want) and int(status) == 0
+        assert (ws.view(torch.int32)[:2 * 16 * 160] == 0).all()
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, 3e38])
+def test_one_head_of_q_that_is_no_ordinary_row(nf, value):
+    """NaN, an infinity or the largest numbers in one head's q: the other heads are as ever."""
+    c = Cache([300, 20], 2, 128, seed=41)
+    q = _dev(np.random.default_rng(7).standard_normal((2, 10, 128)).astype(np.float32), torch.bfloat16)
+    want = _run(nf, c, q)
+    odd = q.clone()
+    odd[:, 7, 40] = value
+    out = _run(nf, c, odd)
+    others = [h for h in range(10) if h != 7]
+    keep = q.clone()
+    keep[:, 7] = 0
+    _check(c, keep, torch.where(torch.arange(10, device="cuda").view(1, 10, 1) == 7, _run(nf, c, keep), out))
+    assert torch.equal(out[:, :5], want[:, :5])     # another KV head: the same bits
+    assert out[:, others].isfinite().all() and (math.isfinite(value) or out[:, 7].isnan().all())
