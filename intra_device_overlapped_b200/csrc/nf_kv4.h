@@ -22,7 +22,6 @@
 namespace nf {
 
 constexpr int kKv4Slots = 16;   // slots per page
-constexpr int kKv4Group = 32;   // columns per scale
 constexpr int kKv4MaxHeads = 256;
 
 __host__ __device__ constexpr int kv4_tile_bytes(int d) { return 9 * d; }

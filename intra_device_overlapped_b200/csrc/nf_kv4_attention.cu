@@ -546,11 +546,11 @@ __device__ __noinline__ void join_parts(const Kv4AttnArgs& a, const Item& it, in
 // Parts of one pair meet in the workspace; a worker reports its parts, two at most, when its share is done, and whoever
 // brings the last one joins them, in order.
 //
-// Measured, calls back to back: 512 requests of 1024 to 1536 keys, 32 query and 8 KV heads of 128: 148 us, 0.79 of a copy
-// of the 761 MB; of 1 to 2048 keys 97.5 us (0.69); 2 of 131072 keys with 64 query heads 67 us (0.66). What bounds it is the
-// turning of codes into operands: about 300 instructions a tile, 60 % of the issue slots and 53 % of the logic pipe in
-// use, with 4 warps a scheduler to cover latencies. To fit 128 registers q's operands are read from shared memory again for
-// every tile; 12 warps of 168 registers hold them and take 153 us.
+// Measured, calls back to back: 512 requests of 1024 to 1536 keys, 32 query and 8 KV heads of 128: 157-165 us on different
+// B200s, 0.70-0.74 of a copy of the 761 MB; of 1 to 2048 keys 101 us (0.67); 2 of 131072 keys with 64 query heads 69 us
+// (0.64). What bounds it is the turning of codes into operands: about 320 instructions a tile, 66 % of the issue slots and
+// 52 % of the logic pipe in use, with 4 warps a scheduler to cover latencies. To fit 128 registers (12 bytes are spilled)
+// q's operands are read from shared memory again for every tile; 12 warps of 168 registers hold them and took 3 % more.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid_constant__ Kv4AttnArgs a) {
     constexpr int NG = D / 32, NW = NG / 2;

@@ -1,6 +1,5 @@
 // Page tables, slot map and positions of a batch built on the GPU from its request lengths.
 #include <cstdint>
-#include <new>
 
 #include <cuda_runtime.h>
 
@@ -101,12 +100,11 @@ __device__ __forceinline__ int row_of(const int* off, int R, int e) {
 
 // With b = ceil(ctx / 16) and a = ceil((ctx + new) / 16) pages of a request before and after, the k-th new
 // page of the batch, in request order, is free_pages[count - 1 - k]. Every CTA scans all R lengths itself
-// (a thread takes R / 1024 consecutive requests; two block scans, first of the pages asked for, then of
-// the pages and tokens granted) and keeps the offsets in shared memory, so no CTA waits for another; the
-// output entries, one per page and one per token, are dealt evenly over all CTAs, each finding its
-// request by bisection. The kernel is bound by latency, not by its few hundred KB:
-// 512 requests of one new token take 6.8 us, 1024, every eighth with a
-// prompt chunk of up to 1024, 7.6.
+// (a thread takes R / 1024 consecutive requests; four block scans of three barriers each, of the pages asked for and,
+// once it is known who gets them, of pages, tokens and pages taken) and keeps the offsets in shared memory, so no CTA
+// waits for another; the output entries, one per page and one per token, are dealt evenly over all CTAs, each finding its
+// request by bisection. The kernel is bound by latency, not by its few hundred KB: 512 requests of one new token take 6.4
+// us, 1024, every eighth with a prompt chunk of up to 1024, 7.6.
 __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const PageMapArgs a) {
     extern __shared__ int sm[];
     int* page_off = sm;                    // [R + 1]
@@ -255,8 +253,6 @@ extern "C" nf_status nf_op_page_map(const int32_t* ctx_len, const int32_t* new_l
                             free_left, status_device};
     nf::page_map_kernel<<<(int)grid, nf::kMapThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
     return cudaGetLastError() == cudaSuccess ? NF_OK : NF_ERR_CUDA;
-} catch (const std::bad_alloc&) {
-    return NF_ERR_OUT_OF_MEMORY;
 } catch (...) {
     return NF_ERR_INVALID_ARGUMENT;
 }

@@ -46,7 +46,8 @@ __device__ __forceinline__ void form_turns(const RopeArgs& a, int t, float2* cs,
 // is read and written once, so the kernel is bound by HBM: 8192 rows of 72 bf16 heads of 128 take 50.7 us, 0.91 of a copy,
 // 8192 of 40 heads from fp32 to bf16 40.1, 0.96. Blocks of 256 threads end soonest where each has an SM nearly for itself,
 // small ones keep more loads in flight and more tokens' turns beside them: with 256, 128 and 64 threads 32 such rows 3.2, 3.9
-// and 5.6 us, 512 5.3, 5.3 and 6.6, 1024 8.5, 7.6 and 8.2, 2048 16, 14.8 and 13.2. (Two vectors a thread at a time: 10 %
+// and 5.6 us, 512 5.3, 5.3 and 6.6, 1024 8.5, 7.6 and 8.2, 2048 16, 14.8 and 13.2. Few heads, 2 of 64 to 9 of 128, change at
+// the same numbers of tokens: 700 2.4, 2.3 and 2.4 us, 2000 4.3, 3.3 and 3.0 (2 of 64). (Two vectors a thread at a time: 10 %
 // more time, for the registers that they hold.)
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const RopeArgs a, const FastDiv per_head) {
