@@ -491,8 +491,8 @@ nf_status nf_decode_attention_noalloc(const void* q, void* out, const void* kv_p
  *
  * Common to these calls: device pointers of the current device (or managed memory; anything else, or a
  * pointer that is not aligned to its elements, is NF_ERR_INVALID_ARGUMENT), row strides in elements between
- * consecutive tokens, head h of a row at column h * head_dim. `status_device` (required) is an int32 that the caller zeroes; it receives the first error
- * that the device finds. All are asynchronous on `stream`, allocate nothing and may be captured into CUDA
+ * consecutive tokens, head h of a row at column h * head_dim. `status_device` (required) is an int32 that the
+ * caller zeroes; it receives the first error that the device finds. All are asynchronous on `stream`, allocate nothing and may be captured into CUDA
  * graphs. NF_ERR_UNSUPPORTED for head dims other than 64 and 128, more than 256 KV heads or more than 8
  * query heads per KV head (nf_op_rope: head dims above 512, more than 65536 heads). */
 

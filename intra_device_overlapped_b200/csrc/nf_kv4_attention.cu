@@ -414,9 +414,9 @@ __device__ __forceinline__ void exact_sums(const Kv4AttnArgs& a, Smem<D>& sm, co
     }
 }
 
-// The rest of the warp's share by exact_sums, from a stretch on whose fp16 weights or q may have lost something (Scores and
-// Output, at the kernel). Returns the parts to be reported. The warp does not come back to the tensor instructions: kept alive across
-// this call, the state of their loop cost registers, and 512 requests of 1280 keys 6 % of their time.
+// The rest of the warp's share by exact_sums, from a stretch on whose fp16 weights or q may have lost something (Scores
+// and Output, at the kernel). Returns the parts to be reported. The warp does not come back to the tensor instructions:
+// kept alive across this call, the state of their loop cost registers, and 512 requests of 1280 keys 6 % of their time.
 template <int D>
 __device__ __noinline__ int exact_rest(const Kv4AttnArgs& a, Smem<D>& s) {
     const int warp = threadIdx.x >> 5;
@@ -781,7 +781,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const __grid
                 s.bias[warp][lane] = make_uint4(term(sum[0], sum[1]), NW == 2 ? term(sum[NG - 2], sum[NG - 1]) : 0,
                                                 __float_as_uint(hs0), __float_as_uint(hs1));
             }
-            for (int left = lost ? 0 : keys - offset() * kKv4Slots; left > 0; left -= step * kKv4Slots) {  // keys from the pair on
+            // `left`: keys from the pair on
+            for (int left = lost ? 0 : keys - offset() * kKv4Slots; left > 0; left -= step * kKv4Slots) {
                 if (flying < kStages) fill(k);  // (a new stretch to begin)
                 if (flying == kStages)
                     cp_async_wait<kStages - 1>();
